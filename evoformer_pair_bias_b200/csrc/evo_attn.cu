@@ -15,6 +15,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "evo_attn.h"
 #include "common.cuh"
@@ -27,6 +28,8 @@
 #include "proj_sm100.cuh"
 #include "trimul_sm100.cuh"
 #include "partials.cuh"
+#include "fp8_rows.cuh"
+#include "fp8_sm100.cuh"
 
 #define EVO_VERSION 10000
 
@@ -355,6 +358,138 @@ evo_status_t launch_contraction(const void* a, const void* bb, void* z, int64_t 
     }
     g_launches += 1;
     return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- 8-bit projection
+bool dtype_ok(evo_dtype_t d) { return d == EVO_DTYPE_BF16 || d == EVO_DTYPE_F32; }
+int64_t elem_bytes(evo_dtype_t d) { return d == EVO_DTYPE_BF16 ? 2 : 4; }
+
+// Whether rows of `cols` elements at pitch `ld` can be moved in 16-byte pieces.
+bool rows_vec(const void* ptr, int64_t cols, int64_t ld, int64_t e) {
+    return !ptr || (aligned(ptr, 16) && cols * e % 16 == 0 && ld * e % 16 == 0);
+}
+// The same, where a pitch that is never stepped along (one row) does not matter.
+bool rows_vec(const void* ptr, int64_t rows, int64_t cols, int64_t ld, int64_t e) {
+    return rows_vec(ptr, cols, rows > 1 ? ld : 0, e);
+}
+
+// How a row is held by warps of 256 columns: nv fragments in each of wpr warps.
+struct RowSplit {
+    int nv, wpr, warps;          // warps per block
+};
+constexpr int64_t kMaxRowCols = 32768;
+RowSplit row_split(int64_t cols) {
+    RowSplit s{1, 1, 8};
+    while ((int64_t)s.wpr * 256 < cols && s.wpr < 32) s.wpr *= 2;
+    while ((int64_t)s.nv * s.wpr * 256 < cols) s.nv *= 2;
+    s.warps = std::max(8, s.wpr);
+    return s;
+}
+
+template <template <typename, bool, int> class L, typename P>
+void by_layout(evo_dtype_t dtype, bool vec, int nv, const P& p) {
+    auto pick = [&](auto t, auto v) {
+        using T = decltype(t);
+        constexpr bool V = decltype(v)::value;
+        switch (nv) {
+            case 1: L<T, V, 1>::launch(p); break;
+            case 2: L<T, V, 2>::launch(p); break;
+            default: L<T, V, 4>::launch(p); break;
+        }
+    };
+    auto with = [&](auto t) { vec ? pick(t, std::true_type{}) : pick(t, std::false_type{}); };
+    dtype == EVO_DTYPE_BF16 ? with(__nv_bfloat16{}) : with(float{});
+}
+
+struct NormLaunch {
+    evo::fp8::NormParams p;
+    RowSplit s;
+    int grid;
+    cudaStream_t stream;
+};
+template <typename T, bool VEC, int NV>
+struct NormKernel {
+    static void launch(const NormLaunch& l) {
+        evo::fp8::add_rms_norm_kernel<T, VEC, NV><<<l.grid, 32 * l.s.warps, 0, l.stream>>>(l.p, l.s.wpr);
+    }
+};
+
+struct NormBwdLaunch {
+    evo::fp8::NormBwdParams p;
+    RowSplit s;
+    int grid;
+    cudaStream_t stream;
+};
+template <typename T, bool VEC, int NV>
+struct NormBwdKernel {
+    static void launch(const NormBwdLaunch& l) {
+        const size_t shm = l.s.warps > l.s.wpr ? (size_t)l.s.warps * NV * 256 * sizeof(float) : 0;
+        evo::fp8::rms_bwd_kernel<T, VEC, NV><<<l.grid, 32 * l.s.warps, shm, l.stream>>>(l.p, l.s.wpr);
+    }
+};
+// Blocks of the norm's backward, each of which leaves one partial row of d_weight: a pure
+// function of the sizes, because the workspace query answers from it.
+int64_t norm_bwd_blocks(int64_t rows, int64_t cols) {
+    const RowSplit s = row_split(cols);
+    const int64_t per = s.warps / s.wpr;
+    return std::min<int64_t>((rows + per - 1) / per, 148 * (32 / s.warps));
+}
+
+template <typename T, bool VEC>
+void launch_quantize(const evo::fp8::QuantParams& p, bool square, bool transpose, cudaStream_t s) {
+    if (!square && !transpose) {
+        const int64_t items = p.rows * ((p.cols + 255) / 256);
+        const int grid = (int)std::min<int64_t>((items + 7) / 8, (int64_t)148 * 64);
+        evo::fp8::quantize_rows_kernel<T, VEC><<<grid, 256, 0, s>>>(p);
+        return;
+    }
+    const unsigned grid = (unsigned)((p.rows + 127) / 128 * ((p.cols + 127) / 128));
+    if (!transpose)
+        evo::fp8::quantize_tile_kernel<T, VEC, true, false><<<grid, 512, 0, s>>>(p);
+    else if (square)
+        evo::fp8::quantize_tile_kernel<T, VEC, true, true><<<grid, 512, 0, s>>>(p);
+    else
+        evo::fp8::quantize_tile_kernel<T, VEC, false, true><<<grid, 512, 0, s>>>(p);
+}
+
+// Dynamic shared memory above 48 KB is granted per kernel and device.
+template <typename K>
+bool grant_smem(K kernel, int bytes, std::atomic<uint64_t>* granted) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return false;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (granted[dev >> 6].load() & bit) return true;
+    if (set_smem(kernel, bytes) != cudaSuccess) return false;
+    granted[dev >> 6].fetch_or(bit);
+    return true;
+}
+
+template <typename T, bool SW_ROWS>
+evo_status_t launch_linear(const CUtensorMap* maps, const evo::fp8::LinParams& p, cudaStream_t stream) {
+    namespace sp = evo::fp8::split;
+    auto kern = sp::linear_kernel<T, SW_ROWS>;
+    static std::atomic<uint64_t> granted[4];
+    if (!grant_smem(kern, sp::SMEM, granted)) return EVO_ERR_CUDA;
+    const int64_t tiles = (int64_t)((p.M + evo::fp8::BM - 1) / evo::fp8::BM) * ((p.N + sp::BN - 1) / sp::BN);
+    const int64_t blocks = (p.K + evo::fp8::BK - 1) / evo::fp8::BK;
+    // tiles that leave SMs without work are cut along the summed axis, at least two blocks each
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= sm_count() && blocks >= 4 * S) S *= 2;
+    if (tiles * S > 0x7fffffff) return EVO_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * S));
+    cfg.blockDim = dim3(sp::THREADS);
+    cfg.dynamicSmemBytes = sp::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], p);
+    g_launches += 1;
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
 
 }  // namespace
@@ -686,6 +821,144 @@ evo_status_t evo_attn_bwd_noalloc(const evo_shape_t* shape, evo_dtype_t dtype, c
     if (wst != EVO_OK) return wst;
     return evo_attn_bwd(shape, dtype, q, k, v, g, in_str, mask_bias, pair_bias, out, out_lo, dout, out_str, lse,
                         dq, dk, dv, dg, grad_str, d_pair_bias, ws, EVO_ATTN_NOALLOC_WORKSPACE_BYTES, stream);
+}
+
+evo_status_t evo_add_rms_norm_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx,
+                                  const void* residual, int64_t ldr, const void* weight, evo_dtype_t w_dtype,
+                                  float eps, void* q, int64_t ldq, float* scale, int64_t scale_row,
+                                  int64_t scale_group, void* h, int64_t ldh, void* n, int64_t ldn, float* rstd,
+                                  void* stream) {
+    if (rows < 0 || cols < 1 || !dtype_ok(dtype) || !dtype_ok(w_dtype) || !(eps >= 0.f)) return EVO_ERR_INVALID_ARG;
+    if (rows == 0) return EVO_OK;
+    if (!x || !q || !scale || scale_row < 1 || scale_group < 1) return EVO_ERR_INVALID_ARG;
+    if (ldx < 0 || (residual && ldr < 0) || (rows > 1 && (ldq < cols || (h && ldh < cols) || (n && ldn < cols))))
+        return EVO_ERR_INVALID_ARG;
+    if (cols > kMaxRowCols || !aligned(q, 16) || (rows > 1 && ldq % 16 != 0)) return EVO_ERR_UNSUPPORTED;
+    const int64_t e = elem_bytes(dtype);
+    for (const void* t : {x, residual, (const void*)h, (const void*)n})
+        if (!aligned(t, e)) return EVO_ERR_INVALID_ARG;
+    if (!aligned(weight, elem_bytes(w_dtype)) || !aligned(scale, 4) || !aligned(rstd, 4)) return EVO_ERR_INVALID_ARG;
+    NormLaunch l{};
+    l.p.rows = rows; l.p.cols = cols; l.p.x = x; l.p.res = residual; l.p.ldx = ldx; l.p.ldres = ldr;
+    l.p.w = weight; l.p.w_bf16 = w_dtype == EVO_DTYPE_BF16; l.p.eps = eps;
+    l.p.q = static_cast<uint8_t*>(q); l.p.ldq = ldq;
+    l.p.scale = scale; l.p.s_row = scale_row; l.p.s_grp = scale_group;
+    l.p.h = h; l.p.n = n; l.p.ldh = ldh; l.p.ldn = ldn; l.p.rstd = rstd;
+    l.s = row_split(cols);
+    const int64_t per = l.s.warps / l.s.wpr;
+    l.grid = (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * (64 / l.s.warps));
+    l.stream = static_cast<cudaStream_t>(stream);
+    const bool vec = rows_vec(x, rows, cols, ldx, e) && rows_vec(residual, rows, cols, ldr, e) &&
+                     rows_vec(h, rows, cols, ldh, e) && rows_vec(n, rows, cols, ldn, e);
+    by_layout<NormKernel>(dtype, vec, l.s.nv, l);
+    g_launches += 1;
+    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+size_t evo_add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows < 1 || cols < 1 || cols > kMaxRowCols) return 0;
+    return (size_t)(norm_bwd_blocks(rows, cols) * cols) * sizeof(float);
+}
+
+evo_status_t evo_add_rms_norm_bwd(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* dy, int64_t lddy,
+                                  const void* dh, int64_t lddh, const void* h, int64_t ldh, const float* rstd,
+                                  const void* weight, evo_dtype_t w_dtype, void* dx, int64_t lddx, float* dweight,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    if (rows < 0 || cols < 1 || !dtype_ok(dtype) || !dtype_ok(w_dtype)) return EVO_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!aligned(dweight, 4)) return EVO_ERR_INVALID_ARG;
+    if (cols > kMaxRowCols) return EVO_ERR_UNSUPPORTED;
+    if (rows == 0) {
+        if (dweight && cudaMemsetAsync(dweight, 0, (size_t)cols * sizeof(float), s) != cudaSuccess) return EVO_ERR_CUDA;
+        return EVO_OK;
+    }
+    if (!dy || !h || !rstd || !dx || lddy < 0 || ldh < 0 || (dh && lddh < 0) || (rows > 1 && lddx < cols))
+        return EVO_ERR_INVALID_ARG;
+    const int64_t e = elem_bytes(dtype);
+    for (const void* t : {dy, dh, h, (const void*)dx})
+        if (!aligned(t, e)) return EVO_ERR_INVALID_ARG;
+    if (!aligned(weight, elem_bytes(w_dtype)) || !aligned(rstd, 4)) return EVO_ERR_INVALID_ARG;
+    if (dweight) {
+        if (!workspace || workspace_bytes < evo_add_rms_norm_bwd_workspace_bytes(rows, cols))
+            return EVO_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned(workspace, 16)) return EVO_ERR_INVALID_ARG;
+    }
+    NormBwdLaunch l{};
+    l.p.rows = rows; l.p.cols = cols; l.p.dy = dy; l.p.dh = dh; l.p.h = h;
+    l.p.lddy = lddy; l.p.lddh = lddh; l.p.ldh = ldh; l.p.rstd = rstd;
+    l.p.w = weight; l.p.w_bf16 = w_dtype == EVO_DTYPE_BF16; l.p.dx = dx; l.p.lddx = lddx;
+    l.p.part = dweight ? static_cast<float*>(workspace) : nullptr;
+    l.s = row_split(cols);
+    l.grid = (int)norm_bwd_blocks(rows, cols);
+    l.stream = s;
+    const bool vec = rows_vec(dy, rows, cols, lddy, e) && rows_vec(dh, rows, cols, lddh, e) &&
+                     rows_vec(h, rows, cols, ldh, e) && rows_vec(dx, rows, cols, lddx, e);
+    by_layout<NormBwdKernel>(dtype, vec, l.s.nv, l);
+    g_launches += 1;
+    if (dweight) {
+        evo::fp8::sum_columns_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(l.p.part, l.grid, cols, dweight);
+        g_launches += 1;
+    }
+    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+evo_status_t evo_quantize_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx, int square,
+                              int transpose, void* q, int64_t ldq, float* scale, int64_t scale_row,
+                              int64_t scale_group, void* stream) {
+    if (rows < 0 || cols < 0 || !dtype_ok(dtype)) return EVO_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return EVO_OK;
+    const int64_t q_rows = transpose ? cols : rows, q_cols = transpose ? rows : cols;
+    if (!x || !q || !scale || ldx < 0 || (q_rows > 1 && ldq < q_cols) || scale_row < 1 || scale_group < 1)
+        return EVO_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || (q_rows > 1 && ldq % 16 != 0)) return EVO_ERR_UNSUPPORTED;
+    const int64_t e = elem_bytes(dtype);
+    if (!aligned(x, e) || !aligned(scale, 4)) return EVO_ERR_INVALID_ARG;
+    if ((rows + 127) / 128 > 0x7fffffff / ((cols + 127) / 128)) return EVO_ERR_UNSUPPORTED;
+    evo::fp8::QuantParams p{};
+    p.rows = rows; p.cols = cols; p.x = x; p.ldx = ldx;
+    p.q = static_cast<uint8_t*>(q); p.ldq = ldq; p.scale = scale; p.s_row = scale_row; p.s_grp = scale_group;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool vec = rows_vec(x, rows, cols, ldx, e);
+    if (dtype == EVO_DTYPE_BF16) {
+        if (vec) launch_quantize<__nv_bfloat16, true>(p, square != 0, transpose != 0, s);
+        else launch_quantize<__nv_bfloat16, false>(p, square != 0, transpose != 0, s);
+    } else {
+        if (vec) launch_quantize<float, true>(p, square != 0, transpose != 0, s);
+        else launch_quantize<float, false>(p, square != 0, transpose != 0, s);
+    }
+    g_launches += 1;
+    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const float* x_scale,
+                            int64_t x_scale_row, int64_t x_scale_group, const void* w, int64_t ldw,
+                            const float* w_scale, int64_t w_scale_row, int64_t w_scale_group, int w_scale_rows,
+                            const float* bias, evo_dtype_t y_dtype, void* y, int64_t ldy, void* stream) {
+    if (M < 0 || N < 0 || K < 1 || !dtype_ok(y_dtype)) return EVO_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return EVO_OK;
+    if (!x || !x_scale || !w || !w_scale || !y) return EVO_ERR_INVALID_ARG;
+    if ((M > 1 && (ldx < K || ldy < N)) || (N > 1 && ldw < K)) return EVO_ERR_INVALID_ARG;
+    if (x_scale_row < 0 || x_scale_group < 0 || w_scale_row < 0 || w_scale_group < 0) return EVO_ERR_INVALID_ARG;
+    if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(y, elem_bytes(y_dtype)))
+        return EVO_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || (M > 1 && ldx % 16 != 0) || (N > 1 && ldw % 16 != 0))
+        return EVO_ERR_UNSUPPORTED;
+    const int64_t most = (int64_t)0x7fffffff - 256;
+    if (M > most || N > most || K > most) return EVO_ERR_UNSUPPORTED;
+    CUtensorMap maps[2];
+    std::memset(maps, 0, sizeof(maps));
+    if (!evo::tma::matrix_u8(&maps[0], x, M, K, ldx, evo::fp8::BM) ||
+        !evo::tma::matrix_u8(&maps[1], w, N, K, ldw, evo::fp8::split::BN))
+        return EVO_ERR_CUDA;
+    evo::fp8::LinParams p{};
+    p.M = (int)M; p.N = (int)N; p.K = (int)K;
+    p.sx = x_scale; p.sx_row = x_scale_row; p.sx_grp = x_scale_group;
+    p.sw = w_scale; p.sw_row = w_scale_row; p.sw_grp = w_scale_group;
+    p.bias = bias; p.y = y; p.ldy = ldy;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (y_dtype == EVO_DTYPE_BF16)
+        return w_scale_rows ? launch_linear<__nv_bfloat16, true>(maps, p, s) : launch_linear<__nv_bfloat16, false>(maps, p, s);
+    return w_scale_rows ? launch_linear<float, true>(maps, p, s) : launch_linear<float, false>(maps, p, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,303 @@
+// fp8_sm100.cuh -- the product of two e4m3 matrices with a scale per block of 128
+// along the summed axis, on tcgen05:
+//
+//   y[r,o] = sum_b sx[r,b] * sw[o,b] * (sum_{k in b} x[r,k] w[o,k]) + bias[o]
+//
+// sx has one scale per row and block; sw one per 128 x 128 block (SW_ROWS = false,
+// a layer's weight) or one per row and block (SW_ROWS = true, the operands of a
+// weight's gradient).  The scales are any fp32 numbers, so they cannot enter the
+// tensor core's own block scaling (powers of two): every block's product leaves
+// TMEM once and is added, scaled, into fp32 registers, while the tensor core
+// works on the next block in the other half of TMEM.
+#pragma once
+
+#include "common.cuh"
+#include "sm100.cuh"
+#include "tma_maps.cuh"
+
+namespace evo {
+namespace fp8 {
+
+using namespace evo::sm100;
+
+constexpr int BM = 128;            // rows of y a tile
+constexpr int BK = 128;            // one scale block of the summed axis: 128 bytes, one swizzle span
+enum : unsigned int { kLinTimeout = 0x5000u };
+
+struct LinParams {
+    int M, N, K;                   // y [M, N], summed axis K
+    const float* sx;               // [M, K/128] with strides
+    int64_t sx_row, sx_grp;
+    const float* sw;               // [N or N/128, K/128] with strides
+    int64_t sw_row, sw_grp;
+    const float* bias;             // [N] or null
+    void* y;                       // bf16 or fp32 [M, N]
+    int64_t ldy;
+};
+
+// kind::f8f6f4, e4m3 x e4m3 -> fp32, both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+// ---------------------------------------------------------------- split kernel
+// One 128 x 128 tile of y per cluster; the S CTAs of the cluster each sum a run of
+// blocks, and join their fp32 results through distributed shared memory in rank
+// order (the same bits on every run, one launch, no workspace).  S = 1 where there
+// are tiles enough.  Roles: warp 0 TMA, warp 1 MMA, warps 4-11 add up the blocks
+// (warp % 4 is the quarter of TMEM lanes a warp may read, (warp - 4) / 4 its half
+// of the 128 columns).
+namespace split {
+
+constexpr int BN = 128;
+constexpr int STAGES = 6;
+constexpr int STAGE_BYTES = (BM + BN) * BK;
+constexpr int THREADS = 384;
+constexpr int SWB_OFF = STAGES * STAGE_BYTES;              // 64 column scales for each of 8 warps
+constexpr int BAR_OFF = SWB_OFF + 8 * 64 * 4;
+constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 5) * 8;
+constexpr int SMEM = MISC_OFF + 16 + 1024;
+static_assert(STAGES * STAGE_BYTES >= BM * BN * 4, "the joined tile lies over the stages");
+static_assert(SMEM <= 232448, "shared memory budget");
+
+// float4 chunk `ch` of row `r` of the fp32 tile: chunks permuted by the row, so that lanes
+// holding one chunk of 32 rows, or 32 chunks of one row, meet different banks
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int ch) {
+    return base + (uint32_t)(r * 512 + ((ch ^ (r & 31)) << 4));
+}
+
+template <typename T, bool SW_ROWS>
+__global__ void __launch_bounds__(THREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                  const LinParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = (int)cluster_size(), rank = (int)cluster_rank();
+    const int tile = (int)(blockIdx.x / S), tn = (p.N + BN - 1) / BN;
+    const int m0 = tile / tn * BM, n0 = tile % tn * BN;
+    const int kb_all = (p.K + BK - 1) / BK;
+    const int kb0 = (int)((int64_t)kb_all * rank / S), kb1 = (int)((int64_t)kb_all * (rank + 1) / S);
+    auto bar_full = [&](int i) { return base + BAR_OFF + 8u * i; };
+    auto bar_empty = [&](int i) { return base + BAR_OFF + 8u * (STAGES + i); };
+    auto bar_accf = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + b); };
+    auto bar_acce = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + 2 + b); };
+    const uint32_t bar_done = base + BAR_OFF + 8u * (2 * STAGES + 4);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + MISC_OFF + 4);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(bar_full(i), 1);
+            mbar_init(bar_empty(i), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_accf(b), 1);
+            mbar_init(bar_acce(b), 8);
+        }
+        mbar_init(bar_done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(base + MISC_OFF, 2 * BN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    float acc[64];
+#pragma unroll
+    for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int row = 32 * quarter + lane;                   // of the tile
+
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tmap(&tm_x);
+            prefetch_tmap(&tm_w);
+            bool ok = true;
+            int n = 0;
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
+                const int st = n % STAGES;
+                ok = mbar_wait(bar_empty(st), (uint32_t)(((n / STAGES) & 1) ^ 1), abort_flag, kLinTimeout | 0x01);
+                if (!ok) break;
+                const uint32_t dst = base + st * STAGE_BYTES;
+                mbar_arrive_expect_tx(bar_full(st), STAGE_BYTES);
+                tma_load_2d(dst, &tm_x, bar_full(st), kb * BK, m0);
+                tma_load_2d(dst + BM * BK, &tm_w, bar_full(st), kb * BK, n0);
+            }
+            // the loads still in flight land before shared memory is released or reused
+            volatile int no_abort = 0;
+            for (int u = n > STAGES ? n - STAGES : 0; u < n; ++u)
+                mbar_wait(bar_full(u % STAGES), (uint32_t)((u / STAGES) & 1), &no_abort, kLinTimeout | 0x02);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t IDESC = idesc_e4m3(BM, BN);
+            bool ok = true;
+            int n = 0;
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
+                const int st = n % STAGES, b = n & 1;
+                ok = mbar_wait(bar_acce(b), (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag, kLinTimeout | 0x03);
+                if (ok) ok = mbar_wait(bar_full(st), (uint32_t)((n / STAGES) & 1), abort_flag, kLinTimeout | 0x04);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a = base + st * STAGE_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f8(tmem + (uint32_t)(b * BN), smem_desc(a + kk * 32, 16, 1024, kSw128),
+                           smem_desc(a + BM * BK + kk * 32, 16, 1024, kSw128), IDESC, kk > 0 ? 1u : 0u);
+                mma_commit(bar_empty(st));
+                mma_commit(bar_accf(b));
+            }
+            volatile int no_abort = 0;
+            mma_commit(bar_done);
+            mbar_wait(bar_done, 0, &no_abort, kLinTimeout | 0x05);
+        }
+    } else if (warp >= 4) {
+        const bool live = m0 + row < p.M;
+        const float* sx = p.sx + (int64_t)(live ? m0 + row : 0) * p.sx_row;
+        // SW_ROWS: lane l fetches the scales of columns l and 32 + l of this warp's 64, and the warp
+        // shares them through its own slice of shared memory; else one scale for the whole tile
+        const int c_lo = n0 + 64 * half + lane;
+        const float* sw = p.sw + (SW_ROWS ? (int64_t)min(c_lo, p.N - 1) : (int64_t)(n0 / 128)) * p.sw_row;
+        const float* sw_hi = p.sw + (SW_ROWS ? (int64_t)min(c_lo + 32, p.N - 1) : (int64_t)0) * p.sw_row;
+        float* swb = reinterpret_cast<float*>(gbase + SWB_OFF) + 64 * (warp - 4);
+        float a_next = 0.f, w_next = 0.f, h_next = 0.f;
+        if (kb0 < kb1) {
+            a_next = __ldg(sx + kb0 * p.sx_grp);
+            w_next = __ldg(sw + kb0 * p.sw_grp);
+            if (SW_ROWS) h_next = __ldg(sw_hi + kb0 * p.sw_grp);
+        }
+        int n = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+            const int b = n & 1;
+            float f = a_next;
+            if (SW_ROWS) {
+                __syncwarp();                              // the last block's scales have been read
+                swb[lane] = w_next;
+                swb[32 + lane] = h_next;
+                __syncwarp();
+            } else {
+                f *= w_next;
+            }
+            if (kb + 1 < kb1) {
+                a_next = __ldg(sx + (kb + 1) * p.sx_grp);
+                w_next = __ldg(sw + (kb + 1) * p.sw_grp);
+                if (SW_ROWS) h_next = __ldg(sw_hi + (kb + 1) * p.sw_grp);
+            }
+            const bool ok = mbar_wait(bar_accf(b), (uint32_t)((n >> 1) & 1), abort_flag, kLinTimeout | 0x06);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t ta = tmem + (uint32_t)(b * BN + 64 * half) + ((uint32_t)(32 * quarter) << 16);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t v[32];
+                tmem_ld32_sync(ta + 32 * c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float t = __uint_as_float(v[i]);
+                    if (SW_ROWS) t *= swb[32 * c + i];
+                    acc[32 * c + i] = fmaf(t, f, acc[32 * c + i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_acce(b));
+        }
+    }
+    // every load has landed and every MMA is done: the stages take the fp32 tile
+    __syncthreads();
+    if (warp >= 4 && m0 + row < p.M) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sts128(tile_addr(base, row, 16 * half + i), __float_as_uint(acc[4 * i]), __float_as_uint(acc[4 * i + 1]),
+                   __float_as_uint(acc[4 * i + 2]), __float_as_uint(acc[4 * i + 3]));
+    }
+    if (S > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const int rows = min(BM, p.M - m0);
+    T* y = static_cast<T*>(p.y);
+    const bool vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
+    for (int idx = rank * THREADS + (int)threadIdx.x; idx < rows * 32; idx += S * THREADS) {
+        const int r = idx >> 5, ch = idx & 31, c = n0 + 4 * ch;
+        if (c >= p.N) continue;
+        const uint32_t at = tile_addr(base, r, ch);
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < S; ++k) {
+            const float4 v = ld_cluster(at, (uint32_t)k);
+            o[0] += v.x;
+            o[1] += v.y;
+            o[2] += v.z;
+            o[3] += v.w;
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.N) o[e] += __ldg(p.bias + c + e);
+        }
+        T* out = y + (int64_t)(m0 + r) * p.ldy + c;
+        if (vec && c + 4 <= p.N) {
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+            else
+                *reinterpret_cast<float4*>(out) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.N) Elem<T>::store(out + e, o[e]);
+        }
+    }
+    tc_fence_before();
+    if (S > 1)
+        cluster_sync();                                    // peers have read this CTA's tile
+    else
+        __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+}  // namespace split
+}  // namespace fp8
+}  // namespace evo

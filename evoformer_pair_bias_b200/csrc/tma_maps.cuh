@@ -115,6 +115,15 @@ inline bool matrix_bf16(CUtensorMap* m, const void* ptr, int64_t rows, int64_t c
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// 8-bit row-major matrix [rows, cols] with row pitch ld (bytes), viewed as
+// (col, row); box (128 cols, box_rows) with 128B swizzle.
+inline bool matrix_u8(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+    const uint64_t str[1] = {(uint64_t)ld};
+    const uint32_t box[2] = {128, box_rows};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // A stack of `batch` contiguous rows x cols bf16 matrices [batch][rows][cols],
 // boxes of box0 (<= 64, one 128-byte swizzle span) x box1 rows of one matrix.
 inline bool batch_bf16(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_t batch, uint32_t box0,

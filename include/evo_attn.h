@@ -300,6 +300,114 @@ evo_status_t evo_outer_product_mean(int64_t B, int64_t S, int64_t N, int64_t Ca,
 #define EVO_MAX_PARTIALS 64
 evo_status_t evo_sum_partials(int64_t count, const float* const* parts, int64_t n, float* out, void* stream);
 
+/*
+ * The 8-bit projection.  The four calls below take the rows of a residual
+ * stream through a projection in 8-bit floating point and back: the norm in
+ * front of it, the quantiser for weights, other activations and gradients,
+ * the product, and the norm's gradient.  The product's output is bf16 or
+ * fp32, e.g. q, k, v and g of the attention as [B, S, N, H, c] views with row
+ * stride 4*H*c; the same product computes both gradients of the projection
+ * from quantised operands.
+ *
+ * An 8-bit matrix [R, C] is e4m3 with one fp32 scale for each group of 128
+ * columns of a row (1 x 128), or for each block of 128 rows x 128 columns;
+ * the last group or block of an axis may be shorter.  A value is code * scale.
+ * With m the largest magnitude of a group, held at 2^-100 or above,
+ *
+ *   code = e4m3(448 * v / m)      scale = m / 448
+ *
+ * where the quotient is correctly rounded to fp32 and then once to e4m3
+ * (nearest, ties to even).  A group that holds a NaN or an infinity gets a
+ * NaN scale: its products are NaN, as they would be without rounding.
+ *
+ * Codes: rows at a pitch of ld bytes, a multiple of 16, the first 16-byte
+ * aligned (else EVO_ERR_UNSUPPORTED); bytes between C and the pitch are never
+ * written and may hold anything.  Scales: group (r, g) lies at
+ * scale[r * scale_row + g * scale_group], r counting rows (1 x 128) or blocks
+ * of 128 rows.  Any sizes and any strides; fp32 and bf16 matrices whose rows
+ * are 16-byte aligned take 16-byte loads, others single ones.  Stream-ordered,
+ * no allocation, no synchronisation.
+ */
+
+/*
+ * Residual addition, root-mean-square norm and quantisation of its output:
+ *
+ *   h[r,:] = x[r,:] + residual[r,:]                (rounded to the type of x)
+ *   rstd[r] = 1 / sqrt(mean_c(h[r,c]^2) + eps)
+ *   n[r,c] = h[r,c] * rstd[r] * weight[c]
+ *   q, scale = n in e4m3 with 1 x 128 groups
+ *
+ * x, residual: `dtype` [rows, cols] with row pitches ldx, ldr (elements);
+ * residual NULL means zero.  weight: [cols] of w_dtype, or NULL for ones.
+ * q, scale: as above; scale is always written.  h, n: `dtype` [rows, cols] or
+ * NULL (not written); h may be x or residual itself.  rstd: fp32 [rows] or
+ * NULL.  Statistics and products are fp32; n is quantised before it is
+ * rounded to `dtype`.  In the norm the group maximum that is held at 2^-100
+ * is that of n.  A row whose sum of squares overflows fp32 comes out with NaN
+ * scales.  1 <= cols <= 32768 (EVO_ERR_UNSUPPORTED above); rows == 0 is a
+ * no-op.
+ */
+evo_status_t evo_add_rms_norm_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx,
+                                  const void* residual, int64_t ldr, const void* weight, evo_dtype_t w_dtype,
+                                  float eps, void* q, int64_t ldq, float* scale, int64_t scale_row,
+                                  int64_t scale_group, void* h, int64_t ldh, void* n, int64_t ldn, float* rstd,
+                                  void* stream);
+
+/*
+ * Gradients of that norm, with the rounding to 8 bits passed over (dy is the
+ * gradient with respect to n, dh the one that reaches h by the residual
+ * stream, NULL for none):
+ *
+ *   g = dy * weight,  n' = h * rstd
+ *   dx[r,:] = dh[r,:] + rstd[r] * (g - n' * mean_c(g * n'))
+ *   dweight[c] = sum_r dy[r,c] * n'[r,c]
+ *
+ * dx (of dtype) is the gradient of x and of residual alike.  dweight: fp32
+ * [cols], or NULL (not computed, no workspace needed).  The sum over rows has
+ * a fixed order and no atomics: the same bits on every run.  workspace:
+ * evo_add_rms_norm_bwd_workspace_bytes(rows, cols) bytes, 16-byte aligned,
+ * contents arbitrary; calls that may overlap need one each.  rows == 0 sets
+ * dweight to zero.
+ */
+size_t evo_add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+evo_status_t evo_add_rms_norm_bwd(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* dy, int64_t lddy,
+                                  const void* dh, int64_t lddh, const void* h, int64_t ldh, const float* rstd,
+                                  const void* weight, evo_dtype_t w_dtype, void* dx, int64_t lddx, float* dweight,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A matrix x [rows, cols] of `dtype` (row pitch ldx, elements) in e4m3.
+ *   square == 0  1 x 128 groups: along the columns of x, or, transposed,
+ *                along its rows;
+ *   square != 0  128 x 128 blocks.
+ *   transpose    0: q is [rows, cols].  Else q is x^T, [cols, rows], and the
+ *                scales count its rows and groups.
+ * rows == 0 or cols == 0 is a no-op.
+ */
+evo_status_t evo_quantize_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx, int square,
+                              int transpose, void* q, int64_t ldq, float* scale, int64_t scale_row,
+                              int64_t scale_group, void* stream);
+
+/*
+ * y = x @ w^T + bias of two 8-bit matrices x [M, K] and w [N, K]:
+ *
+ *   y[r,o] = sum_b sx[r,b] * sw[o,b] * (sum_{k in b} x[r,k] * w[o,k]) + bias[o]
+ *
+ * with b the blocks of 128 along K.  x has 1 x 128 scales; w has 128 x 128
+ * block scales (w_scale_rows == 0: a layer's weight) or 1 x 128 scales
+ * (w_scale_rows != 0: both operands of a weight's gradient).  Each block's
+ * product is summed by the tensor cores in fp32, the blocks by fp32
+ * fused multiply-adds; bias: fp32 [N] or NULL; y: y_dtype [M, N], row pitch
+ * ldy (elements); only [0:M, 0:N] is written.  The sum's order is fixed: the
+ * same bits on every run.  K >= 1; M == 0 or N == 0 is a no-op.  Waits in the
+ * kernel are bounded, and one that gives up is reported by
+ * evo_attn_device_status.
+ */
+evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const float* x_scale,
+                            int64_t x_scale_row, int64_t x_scale_group, const void* w, int64_t ldw,
+                            const float* w_scale, int64_t w_scale_row, int64_t w_scale_group, int w_scale_rows,
+                            const float* bias, evo_dtype_t y_dtype, void* y, int64_t ldy, void* stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* evo_status_string(evo_status_t status);
 
