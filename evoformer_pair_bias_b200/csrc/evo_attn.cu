@@ -464,18 +464,40 @@ bool grant_smem(K kernel, int bytes, std::atomic<uint64_t>* granted) {
     return true;
 }
 
+// The wide kernel keeps one CTA on each SM and hands registers between its warps, which only
+// works out when it was compiled to the count that the split was written for.
 template <typename T, bool SW_ROWS>
-evo_status_t launch_linear(const CUtensorMap* maps, const evo::fp8::LinParams& p, cudaStream_t stream) {
+evo_status_t launch_linear_wide(CUtensorMap* maps, const evo::fp8::LinParams& p, cudaStream_t stream) {
+    namespace wd = evo::fp8::wide;
+    auto kern = wd::linear_kernel<T, SW_ROWS>;
+    static std::atomic<uint64_t> granted[4];
+    if (!grant_smem(kern, wd::SMEM, granted)) return EVO_ERR_CUDA;
+    static const int regs = [&] {
+        cudaFuncAttributes fa{};
+        return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs != wd::LAUNCH_REGS) return EVO_ERR_CUDA;
+    const int64_t tiles = (int64_t)((p.M + evo::fp8::BM - 1) / evo::fp8::BM) * ((p.N + wd::BN - 1) / wd::BN);
+    if (tiles > 0x7fffffff - 65536) return EVO_ERR_UNSUPPORTED;
+    const int64_t e = sizeof(T);
+    const bool tma_out = aligned(p.y, 16) && (p.M == 1 || p.ldy * e % 16 == 0);
+    if (!evo::tma::matrix_u8(&maps[1], p.w, p.N, p.K, p.ldw, wd::BN)) return EVO_ERR_CUDA;
+    if (tma_out && !evo::tma::boxes_out(&maps[2], p.y, p.M, p.N, p.ldy, (int)e)) return EVO_ERR_CUDA;
+    const int grid = (int)std::min<int64_t>(tiles, sm_count());
+    kern<<<grid, wd::THREADS, wd::SMEM, stream>>>(maps[0], maps[1], maps[2], p, tma_out ? 1 : 0);
+    g_launches += 1;
+    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+template <typename T, bool SW_ROWS>
+evo_status_t launch_linear_split(CUtensorMap* maps, const evo::fp8::LinParams& p, int S, cudaStream_t stream) {
     namespace sp = evo::fp8::split;
     auto kern = sp::linear_kernel<T, SW_ROWS>;
     static std::atomic<uint64_t> granted[4];
     if (!grant_smem(kern, sp::SMEM, granted)) return EVO_ERR_CUDA;
     const int64_t tiles = (int64_t)((p.M + evo::fp8::BM - 1) / evo::fp8::BM) * ((p.N + sp::BN - 1) / sp::BN);
-    const int64_t blocks = (p.K + evo::fp8::BK - 1) / evo::fp8::BK;
-    // tiles that leave SMs without work are cut along the summed axis, at least two blocks each
-    int S = 1;
-    while (S < 8 && tiles * S * 2 <= sm_count() && blocks >= 4 * S) S *= 2;
     if (tiles * S > 0x7fffffff) return EVO_ERR_UNSUPPORTED;
+    if (!evo::tma::matrix_u8(&maps[1], p.w, p.N, p.K, p.ldw, sp::BN)) return EVO_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(tiles * S));
     cfg.blockDim = dim3(sp::THREADS);
@@ -490,6 +512,21 @@ evo_status_t launch_linear(const CUtensorMap* maps, const evo::fp8::LinParams& p
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], p);
     g_launches += 1;
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+template <typename T, bool SW_ROWS>
+evo_status_t launch_linear(const evo::fp8::LinParams& p, cudaStream_t stream) {
+    CUtensorMap maps[3];
+    std::memset(maps, 0, sizeof(maps));
+    if (!evo::tma::matrix_u8(&maps[0], p.x, p.M, p.K, p.ldx, evo::fp8::BM)) return EVO_ERR_CUDA;
+    const int64_t tm = (p.M + evo::fp8::BM - 1) / evo::fp8::BM;
+    const int64_t blocks = (p.K + evo::fp8::BK - 1) / evo::fp8::BK;
+    const int64_t tiles = tm * ((p.N + evo::fp8::split::BN - 1) / evo::fp8::split::BN);
+    if (tiles > sm_count()) return launch_linear_wide<T, SW_ROWS>(maps, p, stream);
+    // tiles that leave SMs without work are cut along the summed axis, at least two blocks each
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= sm_count() && blocks >= 4 * S) S *= 2;
+    return launch_linear_split<T, SW_ROWS>(maps, p, S, stream);
 }
 
 }  // namespace
@@ -945,20 +982,16 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
         return EVO_ERR_UNSUPPORTED;
     const int64_t most = (int64_t)0x7fffffff - 256;
     if (M > most || N > most || K > most) return EVO_ERR_UNSUPPORTED;
-    CUtensorMap maps[2];
-    std::memset(maps, 0, sizeof(maps));
-    if (!evo::tma::matrix_u8(&maps[0], x, M, K, ldx, evo::fp8::BM) ||
-        !evo::tma::matrix_u8(&maps[1], w, N, K, ldw, evo::fp8::split::BN))
-        return EVO_ERR_CUDA;
     evo::fp8::LinParams p{};
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
+    p.x = x; p.ldx = ldx; p.w = w; p.ldw = ldw;
     p.sx = x_scale; p.sx_row = x_scale_row; p.sx_grp = x_scale_group;
     p.sw = w_scale; p.sw_row = w_scale_row; p.sw_grp = w_scale_group;
     p.bias = bias; p.y = y; p.ldy = ldy;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (y_dtype == EVO_DTYPE_BF16)
-        return w_scale_rows ? launch_linear<__nv_bfloat16, true>(maps, p, s) : launch_linear<__nv_bfloat16, false>(maps, p, s);
-    return w_scale_rows ? launch_linear<float, true>(maps, p, s) : launch_linear<float, false>(maps, p, s);
+        return w_scale_rows ? launch_linear<__nv_bfloat16, true>(p, s) : launch_linear<__nv_bfloat16, false>(p, s);
+    return w_scale_rows ? launch_linear<float, true>(p, s) : launch_linear<float, false>(p, s);
 }
 
 }  // extern "C"

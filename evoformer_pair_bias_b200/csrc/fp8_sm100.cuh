@@ -26,6 +26,8 @@ enum : unsigned int { kLinTimeout = 0x5000u };
 
 struct LinParams {
     int M, N, K;                   // y [M, N], summed axis K
+    const void *x, *w;             // codes, for the tensor maps
+    int64_t ldx, ldw;
     const float* sx;               // [M, K/128] with strides
     int64_t sx_row, sx_grp;
     const float* sw;               // [N or N/128, K/128] with strides
@@ -299,5 +301,283 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 }  // namespace split
+
+// ----------------------------------------------------------------- wide kernel
+// Persistent, one CTA per SM, 128 x 256 tiles of y, the columns of a row block in
+// succession.  Roles: warp 0 TMA, warp 1 MMA, warps 4-11 add up the blocks and write
+// the tile (warp % 4: the quarter of TMEM lanes; (warp - 4) / 4: the half of the 256
+// columns, one scale block of w).  While they write a tile, the next tile's first two
+// blocks are multiplied.  y leaves through 32-row x 128-byte boxes in shared memory:
+// by TMA where y's rows are 16-byte aligned, else by the warp, a row at a time.
+namespace wide {
+
+constexpr int BN = 256;
+constexpr int STAGES = 4;
+constexpr int STAGE_BYTES = (BM + BN) * BK;
+constexpr int THREADS = 384;
+constexpr int STG_OFF = STAGES * STAGE_BYTES;              // one box for each of 8 warps
+constexpr int BOX = 32 * 128;
+constexpr int BAR_OFF = STG_OFF + 8 * BOX;
+constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 5) * 8;
+constexpr int SMEM = MISC_OFF + 16 + 1024;
+static_assert(SMEM <= 232448, "shared memory budget");
+// registers per thread: 168 at launch (12 warps), handed from the control warps to the others
+constexpr int LAUNCH_REGS = 168, CTRL_REGS = 56, SUM_REGS = 216;
+static_assert(CTRL_REGS + 2 * SUM_REGS <= 3 * LAUNCH_REGS, "register split");
+
+template <typename T, bool SW_ROWS>
+__global__ void __launch_bounds__(THREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                  const __grid_constant__ CUtensorMap tm_y, const LinParams p, const int tma_out) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tn = (p.N + BN - 1) / BN, tiles = (p.M + BM - 1) / BM * tn;
+    const int nkb = (p.K + BK - 1) / BK;
+    auto bar_full = [&](int i) { return base + BAR_OFF + 8u * i; };
+    auto bar_empty = [&](int i) { return base + BAR_OFF + 8u * (STAGES + i); };
+    auto bar_accf = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + b); };
+    auto bar_acce = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + 2 + b); };
+    const uint32_t bar_done = base + BAR_OFF + 8u * (2 * STAGES + 4);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + MISC_OFF + 4);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(bar_full(i), 1);
+            mbar_init(bar_empty(i), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_accf(b), 1);
+            mbar_init(bar_acce(b), 8);
+        }
+        mbar_init(bar_done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(base + MISC_OFF, 2 * BN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        regs_decrease<CTRL_REGS>();
+        if (warp == 0 && lane == 0) {
+            prefetch_tmap(&tm_x);
+            prefetch_tmap(&tm_w);
+            bool ok = true;
+            uint32_t n = 0;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const int m0 = t / tn * BM, n0 = t % tn * BN;
+                for (int kb = 0; ok && kb < nkb; ++kb, ++n) {
+                    const uint32_t st = n % STAGES;
+                    ok = mbar_wait(bar_empty(st), ((n / STAGES) & 1) ^ 1, abort_flag, kLinTimeout | 0x11);
+                    if (!ok) break;
+                    const uint32_t dst = base + st * STAGE_BYTES;
+                    mbar_arrive_expect_tx(bar_full(st), STAGE_BYTES);
+                    tma_load_2d(dst, &tm_x, bar_full(st), kb * BK, m0);
+                    tma_load_2d(dst + BM * BK, &tm_w, bar_full(st), kb * BK, n0);
+                }
+            }
+            // the loads still in flight land before shared memory is released
+            volatile int no_abort = 0;
+            for (uint32_t u = n > STAGES ? n - STAGES : 0; u < n; ++u)
+                mbar_wait(bar_full(u % STAGES), (u / STAGES) & 1, &no_abort, kLinTimeout | 0x12);
+        } else if (warp == 1 && lane == 0) {
+            constexpr uint32_t IDESC = idesc_e4m3(BM, BN);
+            bool ok = true;
+            uint32_t n = 0;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                for (int kb = 0; kb < nkb; ++kb, ++n) {
+                    const uint32_t st = n % STAGES, b = n & 1;
+                    ok = mbar_wait(bar_acce(b), ((n >> 1) & 1) ^ 1, abort_flag, kLinTimeout | 0x13);
+                    if (ok) ok = mbar_wait(bar_full(st), (n / STAGES) & 1, abort_flag, kLinTimeout | 0x14);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = base + st * STAGE_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8(tmem + b * BN, smem_desc(a + kk * 32, 16, 1024, kSw128),
+                               smem_desc(a + BM * BK + kk * 32, 16, 1024, kSw128), IDESC, kk > 0 ? 1u : 0u);
+                    mma_commit(bar_empty(st));
+                    mma_commit(bar_accf(b));
+                }
+            }
+            volatile int no_abort = 0;
+            mma_commit(bar_done);
+            mbar_wait(bar_done, 0, &no_abort, kLinTimeout | 0x15);
+        }
+    } else {
+        regs_increase<SUM_REGS>();
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t stg = base + STG_OFF + (uint32_t)(warp - 4) * BOX;
+        float* swb = reinterpret_cast<float*>(gbase + STG_OFF + (warp - 4) * BOX);   // 128 column scales, in the box
+        if (lane == 0) prefetch_tmap(&tm_y);
+        constexpr int WS = SW_ROWS ? 4 : 1;                // scales of w a lane fetches a block
+        // Scales are fetched two blocks ahead, across tiles: position (ft, fk)
+        int ft = blockIdx.x, fk = 0;
+        const float *fx = p.sx, *fw[WS];
+        auto aim = [&]() {                                 // the scale rows of tile ft
+            const int row = ft / tn * BM + 32 * quarter + lane, c0 = ft % tn * BN + 128 * half;
+            fx = p.sx + (int64_t)min(row, p.M - 1) * p.sx_row;
+#pragma unroll
+            for (int i = 0; i < WS; ++i)
+                fw[i] = p.sw + (int64_t)(SW_ROWS ? min(c0 + lane + 32 * i, p.N - 1) : min(c0, p.N - 1) / 128) * p.sw_row;
+        };
+        float a_q[2] = {0.f, 0.f}, w_q[2][WS];
+        auto fetch = [&](int slot) {
+            if (ft >= tiles) return;
+            a_q[slot] = __ldg(fx + fk * p.sx_grp);
+#pragma unroll
+            for (int i = 0; i < WS; ++i) w_q[slot][i] = __ldg(fw[i] + fk * p.sw_grp);
+            if (++fk == nkb) {
+                fk = 0;
+                ft += gridDim.x;
+                if (ft < tiles) aim();
+            }
+        };
+        if (ft < tiles) aim();
+        fetch(0);
+        fetch(1);
+        bool ok = true;
+        uint32_t n = 0;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            uint64_t acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0;
+            if (SW_ROWS && lane == 0) bulk_wait_read<0>(); // the last tile has left the box
+#pragma unroll 1
+            for (int kb = 0; kb < nkb; ++kb, ++n) {
+                const uint32_t b = n & 1;
+                float f = a_q[0];
+                if (SW_ROWS) {
+                    __syncwarp();                          // the last block's scales have been read
+#pragma unroll
+                    for (int i = 0; i < WS; ++i) swb[lane + 32 * i] = w_q[0][i];
+                    __syncwarp();
+                } else {
+                    f *= w_q[0][0];
+                }
+                a_q[0] = a_q[1];
+#pragma unroll
+                for (int i = 0; i < WS; ++i) w_q[0][i] = w_q[1][i];
+                fetch(1);
+                const uint64_t f2v = f2(f, f);
+                ok = mbar_wait(bar_accf(b), (n >> 1) & 1, abort_flag, kLinTimeout | 0x16);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ta = tmem + b * BN + (uint32_t)(128 * half) + ((uint32_t)(32 * quarter) << 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32_sync(ta + 32 * c, v);
+                    if (c == 3) {                          // everything has been read: the buffer is free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_acce(b));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        uint64_t t0 = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        uint64_t t1 = f2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                        if (SW_ROWS) {
+                            const float4 s = *reinterpret_cast<const float4*>(swb + 32 * c + i);
+                            t0 = fmul2(t0, f2(s.x, s.y));
+                            t1 = fmul2(t1, f2(s.z, s.w));
+                        }
+                        acc[16 * c + i / 2] = ffma2(t0, f2v, acc[16 * c + i / 2]);
+                        acc[16 * c + i / 2 + 1] = ffma2(t1, f2v, acc[16 * c + i / 2 + 1]);
+                    }
+                }
+            }
+            if (!ok) break;
+            // ------------------------------------------------ the tile leaves
+            constexpr int CPB = 128 / sizeof(T);           // columns a box
+            const int row0 = t / tn * BM + 32 * quarter, col0 = t % tn * BN + 128 * half;
+#pragma unroll
+            for (int g = 0; g < 128 / CPB; ++g) {
+                const int c0 = col0 + g * CPB;
+                if (tma_out) {
+                    if (lane == 0) bulk_wait_read<0>();    // the store that last read the box is done with it
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {           // 16-byte chunks of this lane's row
+                    constexpr int E = 16 / sizeof(T);
+                    float o[E];
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const uint64_t a = acc[(g * CPB + ch * E + e) / 2];
+                        o[e] = f2lo(a);
+                        o[e + 1] = f2hi(a);
+                    }
+                    if (p.bias) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) o[e] += __ldg(p.bias + min(c0 + ch * E + e, p.N - 1));
+                    }
+                    const uint32_t at = stg + lane * 128 + ((ch ^ (lane & 7)) << 4);
+                    if constexpr (sizeof(T) == 2)
+                        sts128(at, pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+                    else
+                        sts128(at, __float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3]));
+                }
+                if (tma_out) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && row0 < p.M && c0 < p.N) {
+                        tma_store_2d(&tm_y, stg, c0, row0);
+                        bulk_commit();
+                    }
+                } else {
+                    __syncwarp();
+                    const int rows = min(32, p.M - row0);
+                    for (int r = 0; r < rows; ++r) {
+                        uint32_t v;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v)
+                                     : "r"(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4));
+                        T* out = static_cast<T*>(p.y) + (int64_t)(row0 + r) * p.ldy + c0;
+                        if constexpr (sizeof(T) == 4) {
+                            if (c0 + lane < p.N) out[lane] = __uint_as_float(v);
+                        } else {
+                            uint16_t* o16 = reinterpret_cast<uint16_t*>(out);
+                            const int c = c0 + 2 * lane;
+                            const uint32_t next = __shfl_down_sync(0xffffffffu, v, 1);
+                            if ((reinterpret_cast<uintptr_t>(out) & 3) == 0) {
+                                if (c + 1 < p.N)
+                                    *reinterpret_cast<uint32_t*>(o16 + 2 * lane) = v;
+                                else if (c < p.N)
+                                    o16[2 * lane] = (uint16_t)v;
+                            } else {                       // pairs start at odd columns
+                                if (lane == 0 && c < p.N) o16[0] = (uint16_t)v;
+                                if (lane < 31 && c + 2 < p.N)
+                                    *reinterpret_cast<uint32_t*>(o16 + 2 * lane + 1) = (v >> 16) | (next << 16);
+                                else if (c + 1 < p.N)
+                                    o16[2 * lane + 1] = (uint16_t)(v >> 16);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) bulk_wait<0>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+}  // namespace wide
 }  // namespace fp8
 }  // namespace evo
