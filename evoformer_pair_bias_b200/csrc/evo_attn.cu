@@ -466,12 +466,12 @@ bool grant_smem(K kernel, int bytes, std::atomic<uint64_t>* granted) {
 
 // The wide kernel keeps one CTA on each SM and hands registers between its warps, which only
 // works out when it was compiled to the count that the split was written for.
-template <typename T, bool SW_ROWS>
+template <typename T, bool SW_ROWS, class L>
 evo_status_t launch_linear_wide(CUtensorMap* maps, const evo::fp8::LinParams& p, cudaStream_t stream) {
     namespace wd = evo::fp8::wide;
-    auto kern = wd::linear_kernel<T, SW_ROWS>;
+    auto kern = wd::linear_kernel<T, SW_ROWS, L>;
     static std::atomic<uint64_t> granted[4];
-    if (!grant_smem(kern, wd::SMEM, granted)) return EVO_ERR_CUDA;
+    if (!grant_smem(kern, L::smem, granted)) return EVO_ERR_CUDA;
     static const int regs = [&] {
         cudaFuncAttributes fa{};
         return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
@@ -482,9 +482,9 @@ evo_status_t launch_linear_wide(CUtensorMap* maps, const evo::fp8::LinParams& p,
     const int64_t e = sizeof(T);
     const bool tma_out = aligned(p.y, 16) && (p.M == 1 || p.ldy * e % 16 == 0);
     if (!evo::tma::matrix_u8(&maps[1], p.w, p.N, p.K, p.ldw, wd::BN)) return EVO_ERR_CUDA;
-    if (tma_out && !evo::tma::boxes_out(&maps[2], p.y, p.M, p.N, p.ldy, (int)e)) return EVO_ERR_CUDA;
+    if (tma_out && !evo::tma::boxes_out(&maps[2], p.y, p.M, p.N, p.ldy, (int)e, L::box_cols)) return EVO_ERR_CUDA;
     const int grid = (int)std::min<int64_t>(tiles, sm_count());
-    kern<<<grid, wd::THREADS, wd::SMEM, stream>>>(maps[0], maps[1], maps[2], p, tma_out ? 1 : 0);
+    kern<<<grid, wd::THREADS, L::smem, stream>>>(maps[0], maps[1], maps[2], p, tma_out ? 1 : 0);
     g_launches += 1;
     return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
@@ -522,7 +522,9 @@ evo_status_t launch_linear(const evo::fp8::LinParams& p, cudaStream_t stream) {
     const int64_t tm = (p.M + evo::fp8::BM - 1) / evo::fp8::BM;
     const int64_t blocks = (p.K + evo::fp8::BK - 1) / evo::fp8::BK;
     const int64_t tiles = tm * ((p.N + evo::fp8::split::BN - 1) / evo::fp8::split::BN);
-    if (tiles > sm_count()) return launch_linear_wide<T, SW_ROWS>(maps, p, stream);
+    namespace wd = evo::fp8::wide;
+    if (tiles > sm_count())
+        return launch_linear_wide<T, SW_ROWS, wd::Short>(maps, p, stream);
     // tiles that leave SMs without work are cut along the summed axis, at least two blocks each
     int S = 1;
     while (S < 8 && tiles * S * 2 <= sm_count() && blocks >= 4 * S) S *= 2;

@@ -11,6 +11,8 @@
 // works on the next block in the other half of TMEM.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "sm100.cuh"
 #include "tma_maps.cuh"
@@ -304,28 +306,54 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ----------------------------------------------------------------- wide kernel
 // Persistent, one CTA per SM, 128 x 256 tiles of y, the columns of a row block in
-// succession.  Roles: warp 0 TMA, warp 1 MMA, warps 4-11 add up the blocks and write
-// the tile (warp % 4: the quarter of TMEM lanes; (warp - 4) / 4: the half of the 256
-// columns, one scale block of w).  While they write a tile, the next tile's first two
-// blocks are multiplied.  y leaves through 32-row x 128-byte boxes in shared memory:
-// by TMA where y's rows are 16-byte aligned, else by the warp, a row at a time.
+// succession.  Roles: warp 0 TMA, warp 1 MMA, warp 2 the scales of the coming blocks
+// and warp 3 the bias of the coming tile (cp.async into shared memory), warps 4-11
+// add up the blocks and write the tile (warp % 4: the quarter of TMEM lanes;
+// (warp - 4) / 4: the half of the 256 columns, one scale block of w).  While they write
+// a tile, the next tile's first two blocks are multiplied.  y leaves through boxes of
+// 32 rows in shared memory: by TMA where y's rows are 16-byte aligned, else by the
+// warp, a row at a time.
+//
+// The summing warps hold 128 sums each and nothing that comes from global memory:
+// scales or bias fetched into their own registers spilled, and waited for the load
+// at the spill (131072 x 256 x 1024: 107-125 us, against TODO us).
 namespace wide {
 
 constexpr int BN = 256;
-constexpr int STAGES = 4;
 constexpr int STAGE_BYTES = (BM + BN) * BK;
-constexpr int THREADS = 384;
-constexpr int STG_OFF = STAGES * STAGE_BYTES;              // one box for each of 8 warps
-constexpr int BOX = 32 * 128;
-constexpr int BAR_OFF = STG_OFF + 8 * BOX;
-constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 5) * 8;
-constexpr int SMEM = MISC_OFF + 16 + 1024;
-static_assert(SMEM <= 232448, "shared memory budget");
-// registers per thread: 168 at launch (12 warps), handed from the control warps to the others
-constexpr int LAUNCH_REGS = 168, CTRL_REGS = 56, SUM_REGS = 216;
-static_assert(CTRL_REGS + 2 * SUM_REGS <= 3 * LAUNCH_REGS, "register split");
+constexpr int SUM_WARPS = 16;                              // 4 column groups x 4 lane quarters
+constexpr int COLS = 4 * BN / SUM_WARPS;                   // columns a summing warp holds
+constexpr int THREADS = 32 * (4 + SUM_WARPS);
+constexpr int RING = 8;                                    // blocks whose scales are held
+constexpr int SLOT = (BM + BN) * 4;                        // 128 scales of x, then 2 or 256 of w
+// Shared memory: S stages, X boxes of 32 rows x BB bytes for each summing warp.
+template <int S, int X, int BB>
+struct Layout {
+    static constexpr int stages = S, boxes = X, box_cols = BB, box = 32 * BB;
+    static constexpr int stg_off = S * STAGE_BYTES;
+    static constexpr int ring_off = stg_off + SUM_WARPS * X * box;
+    static constexpr int bias_off = ring_off + RING * SLOT;
+    static constexpr int bar_off = bias_off + 2 * BN * 4;
+    static constexpr int n_bars = 2 * S + 2 * RING + 4 + 4 + 1;
+    static constexpr int misc_off = bar_off + n_bars * 8;
+    static constexpr int smem = misc_off + 16 + 1024;
+    static_assert(smem <= 232448, "shared memory budget");
+};
+using Short = Layout<3, 1, 128>;
+// registers per thread: 96 at launch (20 warps), handed from the control warps to the others
+constexpr int LAUNCH_REGS = 96, CTRL_REGS = 32, SUM_REGS = 112;
+static_assert(4 * CTRL_REGS + SUM_WARPS * SUM_REGS <= (4 + SUM_WARPS) * LAUNCH_REGS, "register split");
 
-template <typename T, bool SW_ROWS>
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on `bar` (which counts the arriving threads) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <typename T, bool SW_ROWS, class L>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                   const __grid_constant__ CUtensorMap tm_y, const LinParams p, const int tma_out) {
@@ -333,32 +361,44 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
+    constexpr int STAGES = L::stages;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tn = (p.N + BN - 1) / BN, tiles = (p.M + BM - 1) / BM * tn;
     const int nkb = (p.K + BK - 1) / BK;
-    auto bar_full = [&](int i) { return base + BAR_OFF + 8u * i; };
-    auto bar_empty = [&](int i) { return base + BAR_OFF + 8u * (STAGES + i); };
-    auto bar_accf = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + b); };
-    auto bar_acce = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + 2 + b); };
-    const uint32_t bar_done = base + BAR_OFF + 8u * (2 * STAGES + 4);
-    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + MISC_OFF);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + MISC_OFF + 4);
+    auto bar = [&](int i) { return base + L::bar_off + 8u * i; };
+    auto bar_full = [&](uint32_t i) { return bar(i); };
+    auto bar_empty = [&](uint32_t i) { return bar(STAGES + i); };
+    auto bar_sfull = [&](uint32_t i) { return bar(2 * STAGES + i); };
+    auto bar_sempty = [&](uint32_t i) { return bar(2 * STAGES + RING + i); };
+    auto bar_accf = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + b); };
+    auto bar_acce = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 2 + b); };
+    auto bar_bfull = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 4 + b); };
+    auto bar_bempty = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 6 + b); };
+    const uint32_t bar_done = bar(2 * STAGES + 2 * RING + 8);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + L::misc_off);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc_off + 4);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(bar_full(i), 1);
             mbar_init(bar_empty(i), 1);
         }
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(bar_sfull(i), 32);
+            mbar_init(bar_sempty(i), SUM_WARPS);
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_accf(b), 1);
-            mbar_init(bar_acce(b), 8);
+            mbar_init(bar_acce(b), SUM_WARPS);
+            mbar_init(bar_bfull(b), 32);
+            mbar_init(bar_bempty(b), SUM_WARPS);
         }
         mbar_init(bar_done, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 0) {
-        tmem_alloc(base + MISC_OFF, 2 * BN);
+        tmem_alloc(base + L::misc_off, 2 * BN);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -368,11 +408,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp < 4) {
         regs_decrease<CTRL_REGS>();
+        bool ok = true;
+        uint32_t n = 0;
         if (warp == 0 && lane == 0) {
             prefetch_tmap(&tm_x);
             prefetch_tmap(&tm_w);
-            bool ok = true;
-            uint32_t n = 0;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 const int m0 = t / tn * BM, n0 = t % tn * BN;
                 for (int kb = 0; ok && kb < nkb; ++kb, ++n) {
@@ -391,8 +431,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_wait(bar_full(u % STAGES), (u / STAGES) & 1, &no_abort, kLinTimeout | 0x12);
         } else if (warp == 1 && lane == 0) {
             constexpr uint32_t IDESC = idesc_e4m3(BM, BN);
-            bool ok = true;
-            uint32_t n = 0;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 for (int kb = 0; kb < nkb; ++kb, ++n) {
                     const uint32_t st = n % STAGES, b = n & 1;
@@ -412,73 +450,73 @@ __global__ void __launch_bounds__(THREADS, 1)
             volatile int no_abort = 0;
             mma_commit(bar_done);
             mbar_wait(bar_done, 0, &no_abort, kLinTimeout | 0x15);
+        } else if (warp == 2) {
+            constexpr int WS = SW_ROWS ? 8 : 1;            // scales of w a lane fetches
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const int m0 = t / tn * BM, n0 = t % tn * BN;
+                const float *fx[4], *fw[WS];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fx[i] = p.sx + (int64_t)min(m0 + lane + 32 * i, p.M - 1) * p.sx_row;
+#pragma unroll
+                for (int i = 0; i < WS; ++i)
+                    fw[i] = p.sw + (int64_t)(SW_ROWS ? min(n0 + lane + 32 * i, p.N - 1)
+                                                     : min(n0 + 128 * (lane & 1), p.N - 1) / 128) * p.sw_row;
+                for (int kb = 0; kb < nkb; ++kb, ++n) {
+                    const uint32_t st = n % RING, dst = base + L::ring_off + st * SLOT + 4 * lane;
+                    ok = mbar_wait(bar_sempty(st), ((n / RING) & 1) ^ 1, abort_flag, kLinTimeout | 0x17);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cp_async4(dst + 128 * i, fx[i] + kb * p.sx_grp);
+#pragma unroll
+                    for (int i = 0; i < WS; ++i)
+                        if (SW_ROWS || lane < 2) cp_async4(dst + 4 * BM + 128 * i, fw[i] + kb * p.sw_grp);
+                    cp_async_arrive(bar_sfull(st));
+                }
+            }
+            cp_async_wait_all();
+        } else if (warp == 3 && p.bias) {
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
+                const int n0 = t % tn * BN;
+                const uint32_t b = n & 1, dst = base + L::bias_off + b * BN * 4 + 4 * lane;
+                ok = mbar_wait(bar_bempty(b), ((n >> 1) & 1) ^ 1, abort_flag, kLinTimeout | 0x18);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) cp_async4(dst + 128 * i, p.bias + min(n0 + lane + 32 * i, p.N - 1));
+                cp_async_arrive(bar_bfull(b));
+            }
+            cp_async_wait_all();
         }
     } else {
         regs_increase<SUM_REGS>();
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t stg = base + STG_OFF + (uint32_t)(warp - 4) * BOX;
-        float* swb = reinterpret_cast<float*>(gbase + STG_OFF + (warp - 4) * BOX);   // 128 column scales, in the box
+        const int quarter = warp & 3, col_w = ((warp - 4) >> 2) * COLS;   // this warp's lanes and columns of the tile
+        const uint32_t stg = base + L::stg_off + (uint32_t)(warp - 4) * L::boxes * L::box;
         if (lane == 0) prefetch_tmap(&tm_y);
-        constexpr int WS = SW_ROWS ? 4 : 1;                // scales of w a lane fetches a block
-        // Scales are fetched two blocks ahead, across tiles: position (ft, fk)
-        int ft = blockIdx.x, fk = 0;
-        const float *fx = p.sx, *fw[WS];
-        auto aim = [&]() {                                 // the scale rows of tile ft
-            const int row = ft / tn * BM + 32 * quarter + lane, c0 = ft % tn * BN + 128 * half;
-            fx = p.sx + (int64_t)min(row, p.M - 1) * p.sx_row;
-#pragma unroll
-            for (int i = 0; i < WS; ++i)
-                fw[i] = p.sw + (int64_t)(SW_ROWS ? min(c0 + lane + 32 * i, p.N - 1) : min(c0, p.N - 1) / 128) * p.sw_row;
-        };
-        float a_q[2] = {0.f, 0.f}, w_q[2][WS];
-        auto fetch = [&](int slot) {
-            if (ft >= tiles) return;
-            a_q[slot] = __ldg(fx + fk * p.sx_grp);
-#pragma unroll
-            for (int i = 0; i < WS; ++i) w_q[slot][i] = __ldg(fw[i] + fk * p.sw_grp);
-            if (++fk == nkb) {
-                fk = 0;
-                ft += gridDim.x;
-                if (ft < tiles) aim();
-            }
-        };
-        if (ft < tiles) aim();
-        fetch(0);
-        fetch(1);
         bool ok = true;
-        uint32_t n = 0;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            uint64_t acc[64];
+        uint32_t n = 0, tile_no = 0;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
+            uint64_t acc[COLS / 2];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
-            if (SW_ROWS && lane == 0) bulk_wait_read<0>(); // the last tile has left the box
+            for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
 #pragma unroll 1
             for (int kb = 0; kb < nkb; ++kb, ++n) {
-                const uint32_t b = n & 1;
-                float f = a_q[0];
-                if (SW_ROWS) {
-                    __syncwarp();                          // the last block's scales have been read
-#pragma unroll
-                    for (int i = 0; i < WS; ++i) swb[lane + 32 * i] = w_q[0][i];
-                    __syncwarp();
-                } else {
-                    f *= w_q[0][0];
-                }
-                a_q[0] = a_q[1];
-#pragma unroll
-                for (int i = 0; i < WS; ++i) w_q[0][i] = w_q[1][i];
-                fetch(1);
-                const uint64_t f2v = f2(f, f);
-                ok = mbar_wait(bar_accf(b), (n >> 1) & 1, abort_flag, kLinTimeout | 0x16);
+                const uint32_t b = n & 1, rs = n % RING;
+                ok = mbar_wait(bar_sfull(rs), (n / RING) & 1, abort_flag, kLinTimeout | 0x19);
+                const float* ring = reinterpret_cast<const float*>(gbase + L::ring_off + rs * SLOT);
+                float f = ring[32 * quarter + lane];
+                if (!SW_ROWS) f *= ring[BM + col_w / 128];
+                if (ok) ok = mbar_wait(bar_accf(b), (n >> 1) & 1, abort_flag, kLinTimeout | 0x16);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ta = tmem + b * BN + (uint32_t)(128 * half) + ((uint32_t)(32 * quarter) << 16);
+                const uint64_t f2v = f2(f, f);
+                const uint32_t ta = tmem + b * BN + (uint32_t)col_w + ((uint32_t)(32 * quarter) << 16);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < COLS / 32; ++c) {
                     uint32_t v[32];
                     tmem_ld32_sync(ta + 32 * c, v);
-                    if (c == 3) {                          // everything has been read: the buffer is free
+                    if (c == COLS / 32 - 1) {              // everything has been read: the buffer is free
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_acce(b));
@@ -488,41 +526,61 @@ __global__ void __launch_bounds__(THREADS, 1)
                         uint64_t t0 = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                         uint64_t t1 = f2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                         if (SW_ROWS) {
-                            const float4 s = *reinterpret_cast<const float4*>(swb + 32 * c + i);
+                            const float4 s = *reinterpret_cast<const float4*>(ring + BM + col_w + 32 * c + i);
                             t0 = fmul2(t0, f2(s.x, s.y));
                             t1 = fmul2(t1, f2(s.z, s.w));
                         }
-                        acc[16 * c + i / 2] = ffma2(t0, f2v, acc[16 * c + i / 2]);
-                        acc[16 * c + i / 2 + 1] = ffma2(t1, f2v, acc[16 * c + i / 2 + 1]);
+                        uint64_t* a = acc + 16 * c + i / 2;
+                        a[0] = ffma2(t0, f2v, a[0]);
+                        a[1] = ffma2(t1, f2v, a[1]);
                     }
                 }
+                __syncwarp();                              // the slot's scales have been read
+                if (lane == 0) mbar_arrive(bar_sempty(rs));
             }
             if (!ok) break;
             // ------------------------------------------------ the tile leaves
-            constexpr int CPB = 128 / sizeof(T);           // columns a box
-            const int row0 = t / tn * BM + 32 * quarter, col0 = t % tn * BN + 128 * half;
+            constexpr int CPB = L::box_cols / sizeof(T), CH = L::box_cols / 16;   // columns, 16-byte chunks a box
+            const int row0 = t / tn * BM + 32 * quarter, col0 = t % tn * BN + col_w;
+            const float* bias_s = reinterpret_cast<const float*>(gbase + L::bias_off) + (tile_no & 1) * BN + col_w;
+            if (p.bias) {
+                ok = mbar_wait(bar_bfull(tile_no & 1), (tile_no >> 1) & 1, abort_flag, kLinTimeout | 0x1a);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+            // chunk `ch` of row `r` in a box, as TMA's swizzle of that width places it
+            auto place = [&](uint32_t box, int r, int ch) {
+                return box + r * L::box_cols + ((ch ^ (L::box_cols == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+            };
 #pragma unroll
-            for (int g = 0; g < 128 / CPB; ++g) {
+            for (int g = 0; g < COLS / CPB; ++g) {
                 const int c0 = col0 + g * CPB;
+                const uint32_t box = stg + (uint32_t)(g % L::boxes) * L::box;
                 if (tma_out) {
-                    if (lane == 0) bulk_wait_read<0>();    // the store that last read the box is done with it
+                    if (lane == 0) bulk_wait_read<L::boxes - 1>();   // the store that last read the box is done with it
                     __syncwarp();
                 }
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {           // 16-byte chunks of this lane's row
+                for (int ch = 0; ch < CH; ++ch) {          // this lane's row
                     constexpr int E = 16 / sizeof(T);
+                    uint64_t o2[E / 2];
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) o2[e] = acc[(g * CPB + ch * E) / 2 + e];
+                    if (p.bias) {
+#pragma unroll
+                        for (int e = 0; e < E; e += 4) {
+                            const float4 v = *reinterpret_cast<const float4*>(bias_s + g * CPB + ch * E + e);
+                            o2[e / 2] = fadd2(o2[e / 2], f2(v.x, v.y));
+                            o2[e / 2 + 1] = fadd2(o2[e / 2 + 1], f2(v.z, v.w));
+                        }
+                    }
                     float o[E];
 #pragma unroll
                     for (int e = 0; e < E; e += 2) {
-                        const uint64_t a = acc[(g * CPB + ch * E + e) / 2];
-                        o[e] = f2lo(a);
-                        o[e + 1] = f2hi(a);
+                        o[e] = f2lo(o2[e / 2]);
+                        o[e + 1] = f2hi(o2[e / 2]);
                     }
-                    if (p.bias) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e) o[e] += __ldg(p.bias + min(c0 + ch * E + e, p.N - 1));
-                    }
-                    const uint32_t at = stg + lane * 128 + ((ch ^ (lane & 7)) << 4);
+                    const uint32_t at = place(box, lane, ch);
                     if constexpr (sizeof(T) == 2)
                         sts128(at, pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
                     else
@@ -531,40 +589,45 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (tma_out) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && row0 < p.M && c0 < p.N) {
-                        tma_store_2d(&tm_y, stg, c0, row0);
-                        bulk_commit();
+                    if (lane == 0) {
+                        if (row0 < p.M && c0 < p.N) tma_store_2d(&tm_y, box, c0, row0);
+                        bulk_commit();                     // also of nothing, so that the wait above keeps its distance
                     }
                 } else {
                     __syncwarp();
-                    const int rows = min(32, p.M - row0);
-                    for (int r = 0; r < rows; ++r) {
+                    constexpr int LPR = L::box_cols / 4;   // lanes a row, one 32-bit word each
+                    const int rows = min(32, p.M - row0), w = lane % LPR;
+                    for (int r = lane / LPR; r < 32; r += 32 / LPR) {
                         uint32_t v;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v)
-                                     : "r"(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4));
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(place(box, r, w >> 2) + (w & 3) * 4));
+                        const uint32_t next = __shfl_down_sync(0xffffffffu, v, 1);
+                        if (r >= rows) continue;
                         T* out = static_cast<T*>(p.y) + (int64_t)(row0 + r) * p.ldy + c0;
                         if constexpr (sizeof(T) == 4) {
-                            if (c0 + lane < p.N) out[lane] = __uint_as_float(v);
+                            if (c0 + w < p.N) out[w] = __uint_as_float(v);
                         } else {
                             uint16_t* o16 = reinterpret_cast<uint16_t*>(out);
-                            const int c = c0 + 2 * lane;
-                            const uint32_t next = __shfl_down_sync(0xffffffffu, v, 1);
+                            const int c = c0 + 2 * w;
                             if ((reinterpret_cast<uintptr_t>(out) & 3) == 0) {
                                 if (c + 1 < p.N)
-                                    *reinterpret_cast<uint32_t*>(o16 + 2 * lane) = v;
+                                    *reinterpret_cast<uint32_t*>(o16 + 2 * w) = v;
                                 else if (c < p.N)
-                                    o16[2 * lane] = (uint16_t)v;
+                                    o16[2 * w] = (uint16_t)v;
                             } else {                       // pairs start at odd columns
-                                if (lane == 0 && c < p.N) o16[0] = (uint16_t)v;
-                                if (lane < 31 && c + 2 < p.N)
-                                    *reinterpret_cast<uint32_t*>(o16 + 2 * lane + 1) = (v >> 16) | (next << 16);
+                                if (w == 0 && c < p.N) o16[0] = (uint16_t)v;
+                                if (w < LPR - 1 && c + 2 < p.N)
+                                    *reinterpret_cast<uint32_t*>(o16 + 2 * w + 1) = (v >> 16) | (next << 16);
                                 else if (c + 1 < p.N)
-                                    o16[2 * lane + 1] = (uint16_t)(v >> 16);
+                                    o16[2 * w + 1] = (uint16_t)(v >> 16);
                             }
                         }
                     }
                     __syncwarp();
                 }
+            }
+            if (p.bias) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_bempty(tile_no & 1));
             }
         }
         if (lane == 0) bulk_wait<0>();
