@@ -464,44 +464,33 @@ bool grant_smem(K kernel, int bytes, std::atomic<uint64_t>* granted) {
     return true;
 }
 
-// The wide kernel keeps one CTA on each SM and hands registers between its warps, which only
-// works out when it was compiled to the count that the split was written for.
+// The kernel hands registers between its warps, which only works out when it was compiled to
+// the count that the split was written for.  S: CTAs that join a tile.
 template <typename T, bool SW_ROWS, class L>
-evo_status_t launch_linear_wide(CUtensorMap* maps, const evo::fp8::LinParams& p, cudaStream_t stream) {
-    namespace wd = evo::fp8::wide;
-    auto kern = wd::linear_kernel<T, SW_ROWS, L>;
+evo_status_t launch_linear_as(const evo::fp8::LinParams& p, int S, cudaStream_t stream) {
+    namespace f8 = evo::fp8;
+    auto kern = f8::linear_kernel<T, SW_ROWS, L>;
     static std::atomic<uint64_t> granted[4];
     if (!grant_smem(kern, L::smem, granted)) return EVO_ERR_CUDA;
     static const int regs = [&] {
         cudaFuncAttributes fa{};
         return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
     }();
-    if (regs != wd::LAUNCH_REGS) return EVO_ERR_CUDA;
-    const int64_t tiles = (int64_t)((p.M + evo::fp8::BM - 1) / evo::fp8::BM) * ((p.N + wd::BN - 1) / wd::BN);
-    if (tiles > 0x7fffffff - 65536) return EVO_ERR_UNSUPPORTED;
+    if (regs != f8::LAUNCH_REGS) return EVO_ERR_CUDA;
+    const int64_t tiles = (int64_t)((p.M + f8::BM - 1) / f8::BM) * ((p.N + L::BN - 1) / L::BN);
+    if (tiles * S > 0x7fffffff - 65536) return EVO_ERR_UNSUPPORTED;
     const int64_t e = sizeof(T);
-    const bool tma_out = aligned(p.y, 16) && (p.M == 1 || p.ldy * e % 16 == 0);
-    if (!evo::tma::matrix_u8(&maps[1], p.w, p.N, p.K, p.ldw, wd::BN)) return EVO_ERR_CUDA;
-    if (tma_out && !evo::tma::boxes_out(&maps[2], p.y, p.M, p.N, p.ldy, (int)e, L::box_cols)) return EVO_ERR_CUDA;
-    const int grid = (int)std::min<int64_t>(tiles, sm_count());
-    kern<<<grid, wd::THREADS, L::smem, stream>>>(maps[0], maps[1], maps[2], p, tma_out ? 1 : 0);
-    g_launches += 1;
-    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
-}
-
-template <typename T, bool SW_ROWS>
-evo_status_t launch_linear_split(CUtensorMap* maps, const evo::fp8::LinParams& p, int S, cudaStream_t stream) {
-    namespace sp = evo::fp8::split;
-    auto kern = sp::linear_kernel<T, SW_ROWS>;
-    static std::atomic<uint64_t> granted[4];
-    if (!grant_smem(kern, sp::SMEM, granted)) return EVO_ERR_CUDA;
-    const int64_t tiles = (int64_t)((p.M + evo::fp8::BM - 1) / evo::fp8::BM) * ((p.N + sp::BN - 1) / sp::BN);
-    if (tiles * S > 0x7fffffff) return EVO_ERR_UNSUPPORTED;
-    if (!evo::tma::matrix_u8(&maps[1], p.w, p.N, p.K, p.ldw, sp::BN)) return EVO_ERR_CUDA;
+    const bool tma_out = !L::JOIN && aligned(p.y, 16) && (p.M == 1 || p.ldy * e % 16 == 0);
+    CUtensorMap maps[3];
+    std::memset(maps, 0, sizeof(maps));
+    if (!evo::tma::matrix_u8(&maps[0], p.x, p.M, p.K, p.ldx, f8::BM) ||
+        !evo::tma::matrix_u8(&maps[1], p.w, p.N, p.K, p.ldw, L::BN) ||
+        (tma_out && !evo::tma::boxes_out(&maps[2], p.y, p.M, p.N, p.ldy, (int)e)))
+        return EVO_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * S));
-    cfg.blockDim = dim3(sp::THREADS);
-    cfg.dynamicSmemBytes = sp::SMEM;
+    cfg.gridDim = dim3((unsigned)(L::JOIN ? tiles * S : std::min<int64_t>(tiles, sm_count())));
+    cfg.blockDim = dim3(f8::THREADS);
+    cfg.dynamicSmemBytes = L::smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -509,26 +498,63 @@ evo_status_t launch_linear_split(CUtensorMap* maps, const evo::fp8::LinParams& p
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], p);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], p, tma_out ? 1 : 0);
     g_launches += 1;
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+    return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+// CTAs of the split kernel that join a tile, 1 to 8: the number whose clusters finish first.  A
+// cluster's CTAs have to lie in one GPC, so the count that run at once is asked for (of 148 SMs:
+// 74 clusters of 2, 33 of 4, 22 of 6, 15 of 8); the answers are kept per device.  Each CTA
+// is left at least two blocks.
+template <typename T, bool SW_ROWS>
+int split_of(int64_t tiles, int64_t blocks) {
+    namespace f8 = evo::fp8;
+    static std::atomic<int> at_once[256][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return 1;
+    int best = 1;
+    double best_t = 0;
+    for (int S = 1; S <= 8 && (S == 1 || blocks >= 2 * S); ++S) {
+        int n = at_once[dev][S].load();
+        if (n == 0) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)S);
+            cfg.blockDim = dim3(f8::THREADS);
+            cfg.dynamicSmemBytes = f8::Split::smem;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)S;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, f8::linear_kernel<T, SW_ROWS, f8::Split>, &cfg) != cudaSuccess || n < 1) {
+                (void)cudaGetLastError();
+                n = -1;
+            }
+            at_once[dev][S].store(n);
+        }
+        if (n < 1) continue;
+        // a CTA's start, join and end cost about as much as six blocks
+        const double t = (double)((tiles + n - 1) / n) * (double)((blocks + S - 1) / S + 6);
+        if (best_t == 0 || t < best_t) {
+            best = S;
+            best_t = t;
+        }
+    }
+    return best;
 }
 
 template <typename T, bool SW_ROWS>
 evo_status_t launch_linear(const evo::fp8::LinParams& p, cudaStream_t stream) {
-    CUtensorMap maps[3];
-    std::memset(maps, 0, sizeof(maps));
-    if (!evo::tma::matrix_u8(&maps[0], p.x, p.M, p.K, p.ldx, evo::fp8::BM)) return EVO_ERR_CUDA;
-    const int64_t tm = (p.M + evo::fp8::BM - 1) / evo::fp8::BM;
-    const int64_t blocks = (p.K + evo::fp8::BK - 1) / evo::fp8::BK;
-    const int64_t tiles = tm * ((p.N + evo::fp8::split::BN - 1) / evo::fp8::split::BN);
-    namespace wd = evo::fp8::wide;
-    if (tiles > sm_count())
-        return launch_linear_wide<T, SW_ROWS, wd::Short>(maps, p, stream);
-    // tiles that leave SMs without work are cut along the summed axis, at least two blocks each
-    int S = 1;
-    while (S < 8 && tiles * S * 2 <= sm_count() && blocks >= 4 * S) S *= 2;
-    return launch_linear_split<T, SW_ROWS>(maps, p, S, stream);
+    namespace f8 = evo::fp8;
+    const int64_t blocks = (p.K + f8::BK - 1) / f8::BK;
+    const int64_t tiles = (int64_t)((p.M + f8::BM - 1) / f8::BM) * ((p.N + f8::Split::BN - 1) / f8::Split::BN);
+    if (tiles > sm_count()) return launch_linear_as<T, SW_ROWS, f8::Wide>(p, 1, stream);
+    static std::atomic<uint64_t> granted[4];               // the occupancy query wants it first
+    if (!grant_smem(f8::linear_kernel<T, SW_ROWS, f8::Split>, f8::Split::smem, granted)) return EVO_ERR_CUDA;
+    const int S = split_of<T, SW_ROWS>(tiles, blocks);
+    return launch_linear_as<T, SW_ROWS, f8::Split>(p, S, stream);
 }
 
 }  // namespace

@@ -75,271 +75,51 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
         : "memory");
     return v;
 }
-// ---------------------------------------------------------------- split kernel
-// One 128 x 128 tile of y per cluster; the S CTAs of the cluster each sum a run of
-// blocks, and join their fp32 results through distributed shared memory in rank
-// order (the same bits on every run, one launch, no workspace).  S = 1 where there
-// are tiles enough.  Roles: warp 0 TMA, warp 1 MMA, warps 4-11 add up the blocks
-// (warp % 4 is the quarter of TMEM lanes a warp may read, (warp - 4) / 4 its half
-// of the 128 columns).
-namespace split {
-
-constexpr int BN = 128;
-constexpr int STAGES = 6;
-constexpr int STAGE_BYTES = (BM + BN) * BK;
-constexpr int THREADS = 384;
-constexpr int SWB_OFF = STAGES * STAGE_BYTES;              // 64 column scales for each of 8 warps
-constexpr int BAR_OFF = SWB_OFF + 8 * 64 * 4;
-constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 5) * 8;
-constexpr int SMEM = MISC_OFF + 16 + 1024;
-static_assert(STAGES * STAGE_BYTES >= BM * BN * 4, "the joined tile lies over the stages");
-static_assert(SMEM <= 232448, "shared memory budget");
-
-// float4 chunk `ch` of row `r` of the fp32 tile: chunks permuted by the row, so that lanes
-// holding one chunk of 32 rows, or 32 chunks of one row, meet different banks
-__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int ch) {
-    return base + (uint32_t)(r * 512 + ((ch ^ (r & 31)) << 4));
-}
-
-template <typename T, bool SW_ROWS>
-__global__ void __launch_bounds__(THREADS, 1)
-    linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                  const LinParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t* gbase = smem_raw + (base - raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = (int)cluster_size(), rank = (int)cluster_rank();
-    const int tile = (int)(blockIdx.x / S), tn = (p.N + BN - 1) / BN;
-    const int m0 = tile / tn * BM, n0 = tile % tn * BN;
-    const int kb_all = (p.K + BK - 1) / BK;
-    const int kb0 = (int)((int64_t)kb_all * rank / S), kb1 = (int)((int64_t)kb_all * (rank + 1) / S);
-    auto bar_full = [&](int i) { return base + BAR_OFF + 8u * i; };
-    auto bar_empty = [&](int i) { return base + BAR_OFF + 8u * (STAGES + i); };
-    auto bar_accf = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + b); };
-    auto bar_acce = [&](int b) { return base + BAR_OFF + 8u * (2 * STAGES + 2 + b); };
-    const uint32_t bar_done = base + BAR_OFF + 8u * (2 * STAGES + 4);
-    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + MISC_OFF);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + MISC_OFF + 4);
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(bar_full(i), 1);
-            mbar_init(bar_empty(i), 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(bar_accf(b), 1);
-            mbar_init(bar_acce(b), 8);
-        }
-        mbar_init(bar_done, 1);
-        *abort_flag = 0;
-        fence_barrier_init();
-    }
-    if (warp == 0) {
-        tmem_alloc(base + MISC_OFF, 2 * BN);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-
-    float acc[64];
-#pragma unroll
-    for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const int row = 32 * quarter + lane;                   // of the tile
-
-    if (warp == 0) {
-        if (lane == 0) {
-            prefetch_tmap(&tm_x);
-            prefetch_tmap(&tm_w);
-            bool ok = true;
-            int n = 0;
-            for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
-                const int st = n % STAGES;
-                ok = mbar_wait(bar_empty(st), (uint32_t)(((n / STAGES) & 1) ^ 1), abort_flag, kLinTimeout | 0x01);
-                if (!ok) break;
-                const uint32_t dst = base + st * STAGE_BYTES;
-                mbar_arrive_expect_tx(bar_full(st), STAGE_BYTES);
-                tma_load_2d(dst, &tm_x, bar_full(st), kb * BK, m0);
-                tma_load_2d(dst + BM * BK, &tm_w, bar_full(st), kb * BK, n0);
-            }
-            // the loads still in flight land before shared memory is released or reused
-            volatile int no_abort = 0;
-            for (int u = n > STAGES ? n - STAGES : 0; u < n; ++u)
-                mbar_wait(bar_full(u % STAGES), (uint32_t)((u / STAGES) & 1), &no_abort, kLinTimeout | 0x02);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t IDESC = idesc_e4m3(BM, BN);
-            bool ok = true;
-            int n = 0;
-            for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
-                const int st = n % STAGES, b = n & 1;
-                ok = mbar_wait(bar_acce(b), (uint32_t)(((n >> 1) & 1) ^ 1), abort_flag, kLinTimeout | 0x03);
-                if (ok) ok = mbar_wait(bar_full(st), (uint32_t)((n / STAGES) & 1), abort_flag, kLinTimeout | 0x04);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t a = base + st * STAGE_BYTES;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_f8(tmem + (uint32_t)(b * BN), smem_desc(a + kk * 32, 16, 1024, kSw128),
-                           smem_desc(a + BM * BK + kk * 32, 16, 1024, kSw128), IDESC, kk > 0 ? 1u : 0u);
-                mma_commit(bar_empty(st));
-                mma_commit(bar_accf(b));
-            }
-            volatile int no_abort = 0;
-            mma_commit(bar_done);
-            mbar_wait(bar_done, 0, &no_abort, kLinTimeout | 0x05);
-        }
-    } else if (warp >= 4) {
-        const bool live = m0 + row < p.M;
-        const float* sx = p.sx + (int64_t)(live ? m0 + row : 0) * p.sx_row;
-        // SW_ROWS: lane l fetches the scales of columns l and 32 + l of this warp's 64, and the warp
-        // shares them through its own slice of shared memory; else one scale for the whole tile
-        const int c_lo = n0 + 64 * half + lane;
-        const float* sw = p.sw + (SW_ROWS ? (int64_t)min(c_lo, p.N - 1) : (int64_t)(n0 / 128)) * p.sw_row;
-        const float* sw_hi = p.sw + (SW_ROWS ? (int64_t)min(c_lo + 32, p.N - 1) : (int64_t)0) * p.sw_row;
-        float* swb = reinterpret_cast<float*>(gbase + SWB_OFF) + 64 * (warp - 4);
-        float a_next = 0.f, w_next = 0.f, h_next = 0.f;
-        if (kb0 < kb1) {
-            a_next = __ldg(sx + kb0 * p.sx_grp);
-            w_next = __ldg(sw + kb0 * p.sw_grp);
-            if (SW_ROWS) h_next = __ldg(sw_hi + kb0 * p.sw_grp);
-        }
-        int n = 0;
-        for (int kb = kb0; kb < kb1; ++kb, ++n) {
-            const int b = n & 1;
-            float f = a_next;
-            if (SW_ROWS) {
-                __syncwarp();                              // the last block's scales have been read
-                swb[lane] = w_next;
-                swb[32 + lane] = h_next;
-                __syncwarp();
-            } else {
-                f *= w_next;
-            }
-            if (kb + 1 < kb1) {
-                a_next = __ldg(sx + (kb + 1) * p.sx_grp);
-                w_next = __ldg(sw + (kb + 1) * p.sw_grp);
-                if (SW_ROWS) h_next = __ldg(sw_hi + (kb + 1) * p.sw_grp);
-            }
-            const bool ok = mbar_wait(bar_accf(b), (uint32_t)((n >> 1) & 1), abort_flag, kLinTimeout | 0x06);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
-            const uint32_t ta = tmem + (uint32_t)(b * BN + 64 * half) + ((uint32_t)(32 * quarter) << 16);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t v[32];
-                tmem_ld32_sync(ta + 32 * c, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float t = __uint_as_float(v[i]);
-                    if (SW_ROWS) t *= swb[32 * c + i];
-                    acc[32 * c + i] = fmaf(t, f, acc[32 * c + i]);
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_acce(b));
-        }
-    }
-    // every load has landed and every MMA is done: the stages take the fp32 tile
-    __syncthreads();
-    if (warp >= 4 && m0 + row < p.M) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            sts128(tile_addr(base, row, 16 * half + i), __float_as_uint(acc[4 * i]), __float_as_uint(acc[4 * i + 1]),
-                   __float_as_uint(acc[4 * i + 2]), __float_as_uint(acc[4 * i + 3]));
-    }
-    if (S > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    const int rows = min(BM, p.M - m0);
-    T* y = static_cast<T*>(p.y);
-    const bool vec = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
-    for (int idx = rank * THREADS + (int)threadIdx.x; idx < rows * 32; idx += S * THREADS) {
-        const int r = idx >> 5, ch = idx & 31, c = n0 + 4 * ch;
-        if (c >= p.N) continue;
-        const uint32_t at = tile_addr(base, r, ch);
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < S; ++k) {
-            const float4 v = ld_cluster(at, (uint32_t)k);
-            o[0] += v.x;
-            o[1] += v.y;
-            o[2] += v.z;
-            o[3] += v.w;
-        }
-        if (p.bias) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < p.N) o[e] += __ldg(p.bias + c + e);
-        }
-        T* out = y + (int64_t)(m0 + r) * p.ldy + c;
-        if (vec && c + 4 <= p.N) {
-            if constexpr (sizeof(T) == 2)
-                *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
-            else
-                *reinterpret_cast<float4*>(out) = make_float4(o[0], o[1], o[2], o[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < p.N) Elem<T>::store(out + e, o[e]);
-        }
-    }
-    tc_fence_before();
-    if (S > 1)
-        cluster_sync();                                    // peers have read this CTA's tile
-    else
-        __syncthreads();
-    if (warp == 0) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, 2 * BN);
-    }
-}
-
-}  // namespace split
-
-// ----------------------------------------------------------------- wide kernel
-// Persistent, one CTA per SM, 128 x 256 tiles of y, the columns of a row block in
-// succession.  Roles: warp 0 TMA, warp 1 MMA, warp 2 the scales of the coming blocks
-// and warp 3 the bias of the coming tile (cp.async into shared memory), warps 4-11
-// add up the blocks and write the tile (warp % 4: the quarter of TMEM lanes;
-// (warp - 4) / 4: the half of the 256 columns, one scale block of w).  While they write
-// a tile, the next tile's first two blocks are multiplied.  y leaves through boxes of
-// 32 rows in shared memory: by TMA where y's rows are 16-byte aligned, else by the
-// warp, a row at a time.
+// ------------------------------------------------------------------ the kernel
+// One CTA per SM, tiles of 128 x BN of y.  Roles: warp 0 TMA, warp 1 MMA, warp 2 the
+// scales of the coming blocks and warp 3 the bias of the coming tile (cp.async into
+// shared memory), warps 4-19 add up the blocks (warp % 4: the quarter of TMEM lanes a
+// warp may read; (warp - 4) / 4: its quarter of the columns) and write the tile.
 //
-// The summing warps hold 128 sums each and nothing that comes from global memory:
-// scales or bias fetched into their own registers spilled, and waited for the load
-// at the spill (131072 x 256 x 1024: 107-125 us, against TODO us).
-namespace wide {
+// Wide   256 columns, persistent: the tiles of a row block in succession.  While one is
+//        written the next one's first two blocks are multiplied.  y leaves through
+//        boxes of 32 rows in shared memory, by TMA where its rows are 16-byte aligned,
+//        else by the warp a row at a time.
+// Split  128 columns, one tile per cluster, for calls with few tiles (few rows, or a
+//        weight's gradient): the CTAs of the cluster each sum a run of blocks and join
+//        their fp32 results through distributed shared memory in rank order -- the same
+//        bits on every run, one launch, no workspace.
+//
+// The summing warps are what bounds the long sums: a block's 128 x BN results are read
+// from TMEM and added in the time the tensor core takes for the next (512 cycles at BN =
+// 256).  Sixteen warps of 64 columns each hide each other's waits; eight of 128 took 335
+// us on 8191 x 4096 x 8192 where sixteen take TODO (the MMAs and loads alone: 180).  They
+// hold their sums and nothing that comes from global memory: scales and bias fetched into
+// their own registers spilled and waited for the load at the spill.
 
-constexpr int BN = 256;
-constexpr int STAGE_BYTES = (BM + BN) * BK;
 constexpr int SUM_WARPS = 16;                              // 4 column groups x 4 lane quarters
-constexpr int COLS = 4 * BN / SUM_WARPS;                   // columns a summing warp holds
 constexpr int THREADS = 32 * (4 + SUM_WARPS);
 constexpr int RING = 8;                                    // blocks whose scales are held
-constexpr int SLOT = (BM + BN) * 4;                        // 128 scales of x, then 2 or 256 of w
-// Shared memory: S stages, X boxes of 32 rows x BB bytes for each summing warp.
-template <int S, int X, int BB>
-struct Layout {
-    static constexpr int stages = S, boxes = X, box_cols = BB, box = 32 * BB;
-    static constexpr int stg_off = S * STAGE_BYTES;
-    static constexpr int ring_off = stg_off + SUM_WARPS * X * box;
+template <int BN_, int STAGES_, bool JOIN_>
+struct Config {
+    static constexpr int BN = BN_, STAGES = STAGES_;
+    static constexpr bool JOIN = JOIN_;                    // a cluster's CTAs join one tile
+    static constexpr int COLS = 4 * BN / SUM_WARPS;        // columns a summing warp holds
+    static constexpr int STAGE_BYTES = (BM + BN) * BK;
+    static constexpr int SLOT = (BM + BN) * 4;             // 128 scales of x, then BN / 128 or BN of w
+    static constexpr int BOX = 32 * 128;                   // JOIN: the tile lies over the stages instead
+    static constexpr int stg_off = STAGES * STAGE_BYTES;
+    static constexpr int ring_off = stg_off + (JOIN ? 0 : SUM_WARPS * BOX);
     static constexpr int bias_off = ring_off + RING * SLOT;
     static constexpr int bar_off = bias_off + 2 * BN * 4;
-    static constexpr int n_bars = 2 * S + 2 * RING + 4 + 4 + 1;
+    static constexpr int n_bars = 2 * STAGES + 2 * RING + 9;
     static constexpr int misc_off = bar_off + n_bars * 8;
     static constexpr int smem = misc_off + 16 + 1024;
     static_assert(smem <= 232448, "shared memory budget");
+    static_assert(!JOIN || (BN == 128 && stg_off >= BM * BN * 4), "the joined tile lies over the stages");
 };
-using Short = Layout<3, 1, 128>;
+using Wide = Config<256, 3, false>;
+using Split = Config<128, 6, true>;
 // registers per thread: 96 at launch (20 warps), handed from the control warps to the others
 constexpr int LAUNCH_REGS = 96, CTRL_REGS = 32, SUM_REGS = 112;
 static_assert(4 * CTRL_REGS + SUM_WARPS * SUM_REGS <= (4 + SUM_WARPS) * LAUNCH_REGS, "register split");
@@ -353,6 +133,12 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// float4 chunk `ch` of row `r` of the joined tile: chunks permuted by the row, so that lanes
+// holding one chunk of 32 rows, or 32 chunks of one row, meet different banks
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int ch) {
+    return base + (uint32_t)(r * 512 + ((ch ^ (r & 31)) << 4));
+}
+
 template <typename T, bool SW_ROWS, class L>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -361,10 +147,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
-    constexpr int STAGES = L::stages;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int BN = L::BN, COLS = L::COLS, STAGES = L::STAGES;
+    // through a shuffle, so that the compiler knows it is the same for the warp (uniform registers)
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int tn = (p.N + BN - 1) / BN, tiles = (p.M + BM - 1) / BM * tn;
-    const int nkb = (p.K + BK - 1) / BK;
+    const int all_kb = (p.K + BK - 1) / BK;
+    // this CTA's tiles t0, t0 + step, ... and of each the blocks kb0 .. kb1 - 1
+    const int S = L::JOIN ? (int)cluster_size() : 1, rank = L::JOIN ? (int)cluster_rank() : 0;
+    const int t0 = (int)blockIdx.x / S, step = L::JOIN ? tiles : (int)gridDim.x;
+    const int kb0 = (int)((int64_t)all_kb * rank / S), kb1 = (int)((int64_t)all_kb * (rank + 1) / S);
     auto bar = [&](int i) { return base + L::bar_off + 8u * i; };
     auto bar_full = [&](uint32_t i) { return bar(i); };
     auto bar_empty = [&](uint32_t i) { return bar(STAGES + i); };
@@ -413,14 +204,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 0 && lane == 0) {
             prefetch_tmap(&tm_x);
             prefetch_tmap(&tm_w);
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = t0; ok && t < tiles; t += step) {
                 const int m0 = t / tn * BM, n0 = t % tn * BN;
-                for (int kb = 0; ok && kb < nkb; ++kb, ++n) {
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
                     const uint32_t st = n % STAGES;
                     ok = mbar_wait(bar_empty(st), ((n / STAGES) & 1) ^ 1, abort_flag, kLinTimeout | 0x11);
                     if (!ok) break;
-                    const uint32_t dst = base + st * STAGE_BYTES;
-                    mbar_arrive_expect_tx(bar_full(st), STAGE_BYTES);
+                    const uint32_t dst = base + st * L::STAGE_BYTES;
+                    mbar_arrive_expect_tx(bar_full(st), L::STAGE_BYTES);
                     tma_load_2d(dst, &tm_x, bar_full(st), kb * BK, m0);
                     tma_load_2d(dst + BM * BK, &tm_w, bar_full(st), kb * BK, n0);
                 }
@@ -431,14 +222,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_wait(bar_full(u % STAGES), (u / STAGES) & 1, &no_abort, kLinTimeout | 0x12);
         } else if (warp == 1 && lane == 0) {
             constexpr uint32_t IDESC = idesc_e4m3(BM, BN);
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                for (int kb = 0; kb < nkb; ++kb, ++n) {
+            for (int t = t0; ok && t < tiles; t += step) {
+                for (int kb = kb0; kb < kb1; ++kb, ++n) {
                     const uint32_t st = n % STAGES, b = n & 1;
                     ok = mbar_wait(bar_acce(b), ((n >> 1) & 1) ^ 1, abort_flag, kLinTimeout | 0x13);
                     if (ok) ok = mbar_wait(bar_full(st), (n / STAGES) & 1, abort_flag, kLinTimeout | 0x14);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = base + st * STAGE_BYTES;
+                    const uint32_t a = base + st * L::STAGE_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8(tmem + b * BN, smem_desc(a + kk * 32, 16, 1024, kSw128),
@@ -451,8 +242,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mma_commit(bar_done);
             mbar_wait(bar_done, 0, &no_abort, kLinTimeout | 0x15);
         } else if (warp == 2) {
-            constexpr int WS = SW_ROWS ? 8 : 1;            // scales of w a lane fetches
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            constexpr int WS = SW_ROWS ? BN / 32 : 1;            // scales of w a lane fetches
+            for (int t = t0; ok && t < tiles; t += step) {
                 const int m0 = t / tn * BM, n0 = t % tn * BN;
                 const float *fx[4], *fw[WS];
 #pragma unroll
@@ -460,9 +251,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < WS; ++i)
                     fw[i] = p.sw + (int64_t)(SW_ROWS ? min(n0 + lane + 32 * i, p.N - 1)
-                                                     : min(n0 + 128 * (lane & 1), p.N - 1) / 128) * p.sw_row;
-                for (int kb = 0; kb < nkb; ++kb, ++n) {
-                    const uint32_t st = n % RING, dst = base + L::ring_off + st * SLOT + 4 * lane;
+                                                     : min(n0 + 128 * (lane & (BN / 128 - 1)), p.N - 1) / 128) * p.sw_row;
+                for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                    const uint32_t st = n % RING, dst = base + L::ring_off + st * L::SLOT + 4 * lane;
                     ok = mbar_wait(bar_sempty(st), ((n / RING) & 1) ^ 1, abort_flag, kLinTimeout | 0x17);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -470,20 +261,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < 4; ++i) cp_async4(dst + 128 * i, fx[i] + kb * p.sx_grp);
 #pragma unroll
                     for (int i = 0; i < WS; ++i)
-                        if (SW_ROWS || lane < 2) cp_async4(dst + 4 * BM + 128 * i, fw[i] + kb * p.sw_grp);
+                        if (SW_ROWS || lane < BN / 128) cp_async4(dst + 4 * BM + 128 * i, fw[i] + kb * p.sw_grp);
                     cp_async_arrive(bar_sfull(st));
                 }
             }
             cp_async_wait_all();
-        } else if (warp == 3 && p.bias) {
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
+        } else if (warp == 3 && p.bias && !L::JOIN) {
+            for (int t = t0; ok && t < tiles; t += step, ++n) {
                 const int n0 = t % tn * BN;
                 const uint32_t b = n & 1, dst = base + L::bias_off + b * BN * 4 + 4 * lane;
                 ok = mbar_wait(bar_bempty(b), ((n >> 1) & 1) ^ 1, abort_flag, kLinTimeout | 0x18);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) cp_async4(dst + 128 * i, p.bias + min(n0 + lane + 32 * i, p.N - 1));
+                for (int i = 0; i < BN / 32; ++i) cp_async4(dst + 128 * i, p.bias + min(n0 + lane + 32 * i, p.N - 1));
                 cp_async_arrive(bar_bfull(b));
             }
             cp_async_wait_all();
@@ -491,19 +282,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         regs_increase<SUM_REGS>();
         const int quarter = warp & 3, col_w = ((warp - 4) >> 2) * COLS;   // this warp's lanes and columns of the tile
-        const uint32_t stg = base + L::stg_off + (uint32_t)(warp - 4) * L::boxes * L::box;
-        if (lane == 0) prefetch_tmap(&tm_y);
+        const uint32_t box = base + L::stg_off + (uint32_t)(warp - 4) * L::BOX;
+        if (!L::JOIN && lane == 0) prefetch_tmap(&tm_y);
         bool ok = true;
         uint32_t n = 0, tile_no = 0;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
+        for (int t = t0; ok && t < tiles; t += step, ++tile_no) {
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
+            const bool live = !L::JOIN || t / tn * BM + 32 * quarter < p.M;   // else no row of y: only arrivals
 #pragma unroll 1
-            for (int kb = 0; kb < nkb; ++kb, ++n) {
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
                 const uint32_t b = n & 1, rs = n % RING;
                 ok = mbar_wait(bar_sfull(rs), (n / RING) & 1, abort_flag, kLinTimeout | 0x19);
-                const float* ring = reinterpret_cast<const float*>(gbase + L::ring_off + rs * SLOT);
+                const float* ring = reinterpret_cast<const float*>(gbase + L::ring_off + rs * L::SLOT);
                 float f = ring[32 * quarter + lane];
                 if (!SW_ROWS) f *= ring[BM + col_w / 128];
                 if (ok) ok = mbar_wait(bar_accf(b), (n >> 1) & 1, abort_flag, kLinTimeout | 0x16);
@@ -512,6 +304,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
                 const uint64_t f2v = f2(f, f);
                 const uint32_t ta = tmem + b * BN + (uint32_t)col_w + ((uint32_t)(32 * quarter) << 16);
+                if (!live) {
+                    if (lane == 0) {
+                        mbar_arrive(bar_acce(b));
+                        mbar_arrive(bar_sempty(rs));
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
                     uint32_t v[32];
@@ -539,8 +338,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(bar_sempty(rs));
             }
             if (!ok) break;
+            if constexpr (L::JOIN) {
+                // the last block's results are there, so every load has landed and every MMA is
+                // done: the stages take the fp32 tile
+                const int row = 32 * quarter + lane;
+                if (t / tn * BM + row < p.M) {
+#pragma unroll
+                    for (int i = 0; i < COLS / 4; ++i)
+                        sts128(tile_addr(base, row, col_w / 4 + i), __float_as_uint(f2lo(acc[2 * i])),
+                               __float_as_uint(f2hi(acc[2 * i])), __float_as_uint(f2lo(acc[2 * i + 1])),
+                               __float_as_uint(f2hi(acc[2 * i + 1])));
+                }
+                break;
+            }
             // ------------------------------------------------ the tile leaves
-            constexpr int CPB = L::box_cols / sizeof(T), CH = L::box_cols / 16;   // columns, 16-byte chunks a box
+            constexpr int CPB = 128 / sizeof(T);           // columns a box
             const int row0 = t / tn * BM + 32 * quarter, col0 = t % tn * BN + col_w;
             const float* bias_s = reinterpret_cast<const float*>(gbase + L::bias_off) + (tile_no & 1) * BN + col_w;
             if (p.bias) {
@@ -548,20 +360,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
             }
-            // chunk `ch` of row `r` in a box, as TMA's swizzle of that width places it
-            auto place = [&](uint32_t box, int r, int ch) {
-                return box + r * L::box_cols + ((ch ^ (L::box_cols == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+            // chunk `ch` of row `r` in a box, as TMA's 128-byte swizzle places it
+            auto place = [&](int r, int ch) {
+                return box + r * 128 + ((ch ^ (r & 7)) << 4);
             };
 #pragma unroll
             for (int g = 0; g < COLS / CPB; ++g) {
                 const int c0 = col0 + g * CPB;
-                const uint32_t box = stg + (uint32_t)(g % L::boxes) * L::box;
                 if (tma_out) {
-                    if (lane == 0) bulk_wait_read<L::boxes - 1>();   // the store that last read the box is done with it
+                    if (lane == 0) bulk_wait_read<0>();    // the store that last read the box is done with it
                     __syncwarp();
                 }
 #pragma unroll
-                for (int ch = 0; ch < CH; ++ch) {          // this lane's row
+                for (int ch = 0; ch < 8; ++ch) {           // this lane's row
                     constexpr int E = 16 / sizeof(T);
                     uint64_t o2[E / 2];
 #pragma unroll
@@ -580,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         o[e] = f2lo(o2[e / 2]);
                         o[e + 1] = f2hi(o2[e / 2]);
                     }
-                    const uint32_t at = place(box, lane, ch);
+                    const uint32_t at = place(lane, ch);
                     if constexpr (sizeof(T) == 2)
                         sts128(at, pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
                     else
@@ -589,19 +400,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (tma_out) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (row0 < p.M && c0 < p.N) tma_store_2d(&tm_y, box, c0, row0);
-                        bulk_commit();                     // also of nothing, so that the wait above keeps its distance
+                    if (lane == 0 && row0 < p.M && c0 < p.N) {
+                        tma_store_2d(&tm_y, box, c0, row0);
+                        bulk_commit();
                     }
                 } else {
                     __syncwarp();
-                    constexpr int LPR = L::box_cols / 4;   // lanes a row, one 32-bit word each
-                    const int rows = min(32, p.M - row0), w = lane % LPR;
-                    for (int r = lane / LPR; r < 32; r += 32 / LPR) {
+                    const int rows = min(32, p.M - row0), w = lane;   // a 32-bit word of the row
+                    for (int r = 0; r < rows; ++r) {
                         uint32_t v;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(place(box, r, w >> 2) + (w & 3) * 4));
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(place(r, w >> 2) + (w & 3) * 4));
                         const uint32_t next = __shfl_down_sync(0xffffffffu, v, 1);
-                        if (r >= rows) continue;
                         T* out = static_cast<T*>(p.y) + (int64_t)(row0 + r) * p.ldy + c0;
                         if constexpr (sizeof(T) == 4) {
                             if (c0 + w < p.N) out[w] = __uint_as_float(v);
@@ -615,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     o16[2 * w] = (uint16_t)v;
                             } else {                       // pairs start at odd columns
                                 if (w == 0 && c < p.N) o16[0] = (uint16_t)v;
-                                if (w < LPR - 1 && c + 2 < p.N)
+                                if (w < 31 && c + 2 < p.N)
                                     *reinterpret_cast<uint32_t*>(o16 + 2 * w + 1) = (v >> 16) | (next << 16);
                                 else if (c + 1 < p.N)
                                     o16[2 * w + 1] = (uint16_t)(v >> 16);
@@ -630,10 +439,49 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(bar_bempty(tile_no & 1));
             }
         }
-        if (lane == 0) bulk_wait<0>();
+        if (!L::JOIN && lane == 0) bulk_wait<0>();
+    }
+    if constexpr (L::JOIN) {
+        const int m0 = t0 / tn * BM, n0 = t0 % tn * BN;
+        cluster_sync();
+        const int rows = min(BM, p.M - m0);
+        T* y = static_cast<T*>(p.y);
+        const bool vec = (p.M == 1 || p.ldy % 4 == 0) && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
+        for (int idx = rank * THREADS + (int)threadIdx.x; idx < rows * 32; idx += S * THREADS) {
+            const int r = idx >> 5, ch = idx & 31, c = n0 + 4 * ch;
+            if (c >= p.N) continue;
+            const uint32_t at = tile_addr(base, r, ch);
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < S; ++k) {
+                const float4 v = ld_cluster(at, (uint32_t)k);
+                o[0] += v.x;
+                o[1] += v.y;
+                o[2] += v.z;
+                o[3] += v.w;
+            }
+            if (p.bias) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.N) o[e] += __ldg(p.bias + c + e);
+            }
+            T* out = y + (int64_t)(m0 + r) * p.ldy + c;
+            if (vec && c + 4 <= p.N) {
+                if constexpr (sizeof(T) == 2)
+                    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+                else
+                    *reinterpret_cast<float4*>(out) = make_float4(o[0], o[1], o[2], o[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.N) Elem<T>::store(out + e, o[e]);
+            }
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if (L::JOIN)
+        cluster_sync();                                    // peers have read this CTA's tile
+    else
+        __syncthreads();
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();
@@ -641,6 +489,5 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-}  // namespace wide
 }  // namespace fp8
 }  // namespace evo

@@ -125,13 +125,13 @@ inline bool matrix_u8(CUtensorMap* m, const void* ptr, int64_t rows, int64_t col
 }
 
 // Row-major output [rows, cols] of 2- or 4-byte elements with row pitch ld (elements), viewed
-// as (col, row); boxes of box_bytes (64 or 128) x 32 rows with the swizzle of that width.
-inline bool boxes_out(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int e, int box_bytes) {
+// as (col, row); boxes of 128 bytes x 32 rows with 128B swizzle.
+inline bool boxes_out(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int e) {
     const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
     const uint64_t str[1] = {(uint64_t)(ld * e)};
-    const uint32_t box[2] = {(uint32_t)(box_bytes / e), 32};
+    const uint32_t box[2] = {(uint32_t)(128 / e), 32};
     return encode(m, e == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (uint32_t)e, ptr, 2,
-                  dims, str, box, box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                  dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // A stack of `batch` contiguous rows x cols bf16 matrices [batch][rows][cols],
