@@ -436,20 +436,48 @@ int64_t norm_bwd_blocks(int64_t rows, int64_t cols) {
 }
 
 template <typename T, bool VEC>
-void launch_quantize(const evo::fp8::QuantParams& p, bool square, bool transpose, cudaStream_t s) {
-    if (!square && !transpose) {
+void launch_quantize(const evo::fp8::QuantParams& p, bool square, cudaStream_t s) {
+    using namespace evo::fp8;
+    if (!square && !p.qt) {
         const int64_t items = p.rows * ((p.cols + 255) / 256);
         const int grid = (int)std::min<int64_t>((items + 7) / 8, (int64_t)148 * 64);
-        evo::fp8::quantize_rows_kernel<T, VEC><<<grid, 256, 0, s>>>(p);
+        quantize_rows_kernel<T, VEC><<<grid, 256, 0, s>>>(p);
         return;
     }
     const unsigned grid = (unsigned)((p.rows + 127) / 128 * ((p.cols + 127) / 128));
-    if (!transpose)
-        evo::fp8::quantize_tile_kernel<T, VEC, true, false><<<grid, 512, 0, s>>>(p);
+    if (!p.qt)
+        quantize_tile_kernel<T, VEC, true, true, false><<<grid, 512, 0, s>>>(p);
+    else if (square && p.q)
+        quantize_tile_kernel<T, VEC, true, true, true><<<grid, 512, 0, s>>>(p);
     else if (square)
-        evo::fp8::quantize_tile_kernel<T, VEC, true, true><<<grid, 512, 0, s>>>(p);
+        quantize_tile_kernel<T, VEC, true, false, true><<<grid, 512, 0, s>>>(p);
+    else if (p.q)
+        quantize_tile_kernel<T, VEC, false, true, true><<<grid, 512, 0, s>>>(p);
     else
-        evo::fp8::quantize_tile_kernel<T, VEC, false, true><<<grid, 512, 0, s>>>(p);
+        quantize_tile_kernel<T, VEC, false, false, true><<<grid, 512, 0, s>>>(p);
+}
+
+// The checks and the launch that evo_quantize_fp8 and evo_quantize_fp8_both share: p.q, p.qt or both.
+evo_status_t quantize(const evo::fp8::QuantParams& p, evo_dtype_t dtype, bool square, cudaStream_t s) {
+    const int64_t e = elem_bytes(dtype);
+    if (!p.x || p.ldx < 0 || !aligned(p.x, e)) return EVO_ERR_INVALID_ARG;
+    auto bad = [](const void* q, int64_t ld, int64_t rows, int64_t cols, const float* sc, int64_t sr, int64_t sg) {
+        return q && (!sc || (rows > 1 && ld < cols) || sr < 1 || sg < 1 || !aligned(sc, 4));
+    };
+    if (bad(p.q, p.ldq, p.rows, p.cols, p.scale, p.s_row, p.s_grp) ||
+        bad(p.qt, p.ldqt, p.cols, p.rows, p.scale_t, p.st_row, p.st_grp))
+        return EVO_ERR_INVALID_ARG;
+    if (!aligned(p.q, 16) || !aligned(p.qt, 16) || (p.q && p.rows > 1 && p.ldq % 16 != 0) ||
+        (p.qt && p.cols > 1 && p.ldqt % 16 != 0))
+        return EVO_ERR_UNSUPPORTED;
+    if ((p.rows + 127) / 128 > 0x7fffffff / ((p.cols + 127) / 128)) return EVO_ERR_UNSUPPORTED;
+    const bool vec = rows_vec(p.x, p.rows, p.cols, p.ldx, e);
+    if (dtype == EVO_DTYPE_BF16)
+        vec ? launch_quantize<__nv_bfloat16, true>(p, square, s) : launch_quantize<__nv_bfloat16, false>(p, square, s);
+    else
+        vec ? launch_quantize<float, true>(p, square, s) : launch_quantize<float, false>(p, square, s);
+    g_launches += 1;
+    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
 
 // Dynamic shared memory above 48 KB is granted per kernel and device.
@@ -927,14 +955,14 @@ size_t evo_add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
 
 evo_status_t evo_add_rms_norm_bwd(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* dy, int64_t lddy,
                                   const void* dh, int64_t lddh, const void* h, int64_t ldh, const float* rstd,
-                                  const void* weight, evo_dtype_t w_dtype, void* dx, int64_t lddx, float* dweight,
-                                  void* workspace, size_t workspace_bytes, void* stream) {
-    if (rows < 0 || cols < 1 || !dtype_ok(dtype) || !dtype_ok(w_dtype)) return EVO_ERR_INVALID_ARG;
+                                  const void* weight, evo_dtype_t w_dtype, void* dx, int64_t lddx, void* dweight,
+                                  evo_dtype_t dw_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (rows < 0 || cols < 1 || !dtype_ok(dtype) || !dtype_ok(w_dtype) || !dtype_ok(dw_dtype)) return EVO_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!aligned(dweight, 4)) return EVO_ERR_INVALID_ARG;
+    if (!aligned(dweight, elem_bytes(dw_dtype))) return EVO_ERR_INVALID_ARG;
     if (cols > kMaxRowCols) return EVO_ERR_UNSUPPORTED;
     if (rows == 0) {
-        if (dweight && cudaMemsetAsync(dweight, 0, (size_t)cols * sizeof(float), s) != cudaSuccess) return EVO_ERR_CUDA;
+        if (dweight && cudaMemsetAsync(dweight, 0, (size_t)(cols * elem_bytes(dw_dtype)), s) != cudaSuccess) return EVO_ERR_CUDA;
         return EVO_OK;
     }
     if (!dy || !h || !rstd || !dx || lddy < 0 || ldh < 0 || (dh && lddh < 0) || (rows > 1 && lddx < cols))
@@ -961,7 +989,11 @@ evo_status_t evo_add_rms_norm_bwd(int64_t rows, int64_t cols, evo_dtype_t dtype,
     by_layout<NormBwdKernel>(dtype, vec, l.s.nv, l);
     g_launches += 1;
     if (dweight) {
-        evo::fp8::sum_columns_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(l.p.part, l.grid, cols, dweight);
+        const unsigned grid = (unsigned)((cols + 31) / 32);
+        if (dw_dtype == EVO_DTYPE_BF16)
+            evo::fp8::sum_columns_kernel<<<grid, 1024, 0, s>>>(l.p.part, l.grid, cols, static_cast<__nv_bfloat16*>(dweight));
+        else
+            evo::fp8::sum_columns_kernel<<<grid, 1024, 0, s>>>(l.p.part, l.grid, cols, static_cast<float*>(dweight));
         g_launches += 1;
     }
     return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
@@ -972,27 +1004,30 @@ evo_status_t evo_quantize_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype, con
                               int64_t scale_group, void* stream) {
     if (rows < 0 || cols < 0 || !dtype_ok(dtype)) return EVO_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return EVO_OK;
-    const int64_t q_rows = transpose ? cols : rows, q_cols = transpose ? rows : cols;
-    if (!x || !q || !scale || ldx < 0 || (q_rows > 1 && ldq < q_cols) || scale_row < 1 || scale_group < 1)
-        return EVO_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || (q_rows > 1 && ldq % 16 != 0)) return EVO_ERR_UNSUPPORTED;
-    const int64_t e = elem_bytes(dtype);
-    if (!aligned(x, e) || !aligned(scale, 4)) return EVO_ERR_INVALID_ARG;
-    if ((rows + 127) / 128 > 0x7fffffff / ((cols + 127) / 128)) return EVO_ERR_UNSUPPORTED;
+    if (!q) return EVO_ERR_INVALID_ARG;
+    evo::fp8::QuantParams p{};
+    p.rows = rows; p.cols = cols; p.x = x; p.ldx = ldx;
+    if (transpose) {
+        p.qt = static_cast<uint8_t*>(q); p.ldqt = ldq; p.scale_t = scale; p.st_row = scale_row; p.st_grp = scale_group;
+    } else {
+        p.q = static_cast<uint8_t*>(q); p.ldq = ldq; p.scale = scale; p.s_row = scale_row; p.s_grp = scale_group;
+    }
+    return quantize(p, dtype, square != 0, static_cast<cudaStream_t>(stream));
+}
+
+evo_status_t evo_quantize_fp8_both(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx,
+                                   int square, void* q, int64_t ldq, float* scale, int64_t scale_row,
+                                   int64_t scale_group, void* q_t, int64_t ldq_t, float* scale_t,
+                                   int64_t scale_t_row, int64_t scale_t_group, void* stream) {
+    if (rows < 0 || cols < 0 || !dtype_ok(dtype)) return EVO_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return EVO_OK;
+    if (!q || !q_t) return EVO_ERR_INVALID_ARG;
     evo::fp8::QuantParams p{};
     p.rows = rows; p.cols = cols; p.x = x; p.ldx = ldx;
     p.q = static_cast<uint8_t*>(q); p.ldq = ldq; p.scale = scale; p.s_row = scale_row; p.s_grp = scale_group;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool vec = rows_vec(x, rows, cols, ldx, e);
-    if (dtype == EVO_DTYPE_BF16) {
-        if (vec) launch_quantize<__nv_bfloat16, true>(p, square != 0, transpose != 0, s);
-        else launch_quantize<__nv_bfloat16, false>(p, square != 0, transpose != 0, s);
-    } else {
-        if (vec) launch_quantize<float, true>(p, square != 0, transpose != 0, s);
-        else launch_quantize<float, false>(p, square != 0, transpose != 0, s);
-    }
-    g_launches += 1;
-    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+    p.qt = static_cast<uint8_t*>(q_t); p.ldqt = ldq_t; p.scale_t = scale_t;
+    p.st_row = scale_t_row; p.st_grp = scale_t_group;
+    return quantize(p, dtype, square != 0, static_cast<cudaStream_t>(stream));
 }
 
 evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const float* x_scale,

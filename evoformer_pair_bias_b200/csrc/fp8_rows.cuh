@@ -390,20 +390,23 @@ __global__ void __launch_bounds__(1024) rms_bwd_kernel(const NormBwdParams p, co
 }
 
 // out[c] = sum over the n partial rows, in a fixed order: 32 threads a column, each every 32nd row.
-__global__ void __launch_bounds__(1024) sum_columns_kernel(const float* part, int64_t n, int64_t cols, float* out) {
+template <typename T>
+__global__ void __launch_bounds__(1024) sum_columns_kernel(const float* part, int64_t n, int64_t cols, T* out) {
     __shared__ float s[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float a = 0.f;
-    if (c < cols)
+    if (c < cols) {
+#pragma unroll 4
         for (int64_t r = ty; r < n; r += 32) a += part[r * cols + c];
+    }
     s[ty][tx] = a;
     __syncthreads();
     a = s[tx][ty];
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     const int64_t cc = (int64_t)blockIdx.x * 32 + ty;
-    if (tx == 0 && cc < cols) out[cc] = a;
+    if (tx == 0 && cc < cols) Elem<T>::store(out + cc, a);
 }
 
 // ------------------------------------------------------------- quantise
@@ -411,10 +414,14 @@ struct QuantParams {
     int64_t rows, cols;          // of x
     const void* x;               // T [rows, cols]
     int64_t ldx;
-    uint8_t* q;                  // e4m3 [rows, cols], or [cols, rows] transposed
+    uint8_t* q;                  // e4m3 [rows, cols]
     int64_t ldq;
-    float* scale;                // [rows of q or blocks, groups] with strides
+    float* scale;                // [rows or blocks, groups] with strides
     int64_t s_row, s_grp;
+    uint8_t* qt;                 // e4m3 [cols, rows], the transpose
+    int64_t ldqt;
+    float* scale_t;              // [cols or blocks, groups] with strides
+    int64_t st_row, st_grp;
 };
 
 // 1 x 128 groups along the rows: a warp takes 256 columns of a row at a time.
@@ -439,112 +446,123 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
 }
 
 // A 128 x 128 tile of x in one block of 512 threads, TC columns x TR rows a thread:
-//   bf16 VEC  8 columns x 4 rows (16-byte loads, 16 lanes a row)
+//   bf16 VEC  8 columns x 4 rows (16-byte loads, 16 lanes a row), kept as loaded
 //   fp32 VEC  4 columns x 8 rows (16-byte loads, a warp a row)
 //   else      columns l + 32j, 8 rows (single loads, a warp a row)
 template <typename T, bool VEC>
 struct Tile {
-    static constexpr int TC = VEC && sizeof(T) == 2 ? 8 : 4;
+    static constexpr bool PACKED = VEC && sizeof(T) == 2;
+    static constexpr int TC = PACKED ? 8 : 4;
     static constexpr int TR = 32 / TC;
     static constexpr int LPR = 128 / TC;         // lanes a row
-    static __device__ __forceinline__ int col(int lane, int j) {
-        return VEC ? (lane % LPR) * TC + j : lane + 32 * j;
-    }
-    static __device__ __forceinline__ int row(int warp, int lane) { return warp * 8 + (lane / LPR) * TR; }
-};
+    uint32_t v[TR][4];                           // four bf16 pairs or four floats
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_tile(const QuantParams& p, int64_t r0, int64_t c0, int warp, int lane,
-                                          float (*v)[Tile<T, VEC>::TC]) {
-    using L = Tile<T, VEC>;
-    const int64_t r = r0 + L::row(warp, lane);
+    static __device__ __forceinline__ int col(int lane, int j) { return VEC ? (lane % LPR) * TC + j : lane + 32 * j; }
+    static __device__ __forceinline__ int row(int warp, int lane) { return warp * 8 + (lane / LPR) * TR; }
+
+    __device__ __forceinline__ void load(const QuantParams& p, int64_t r0, int64_t c0, int warp, int lane) {
+        const int64_t r = r0 + row(warp, lane);
 #pragma unroll
-    for (int i = 0; i < L::TR; ++i) {
-        const T* row = static_cast<const T*>(p.x) + (r + i) * p.ldx;
-        const bool live = r + i < p.rows;
-        if constexpr (VEC) {
-            const int64_t c = c0 + L::col(lane, 0);
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live && c < p.cols) w = *reinterpret_cast<const uint4*>(row + c);
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-            if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[i][2 * e] = sm100::bf16lo(a[e]);
-                    v[i][2 * e + 1] = sm100::bf16hi(a[e]);
-                }
+        for (int i = 0; i < TR; ++i) {
+            const T* x = static_cast<const T*>(p.x) + (r + i) * p.ldx;
+            const bool live = r + i < p.rows;
+            if constexpr (VEC) {
+                const int64_t c = c0 + col(lane, 0);
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (live && c < p.cols) w = *reinterpret_cast<const uint4*>(x + c);
+                v[i][0] = w.x;
+                v[i][1] = w.y;
+                v[i][2] = w.z;
+                v[i][3] = w.w;
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i][e] = __uint_as_float(a[e]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t c = c0 + L::col(lane, j);
-                v[i][j] = live && c < p.cols ? Elem<T>::load(row + c) : 0.f;
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t c = c0 + col(lane, j);
+                    v[i][j] = live && c < p.cols ? __float_as_uint(Elem<T>::load(x + c)) : 0u;
+                }
             }
         }
     }
-}
+    __device__ __forceinline__ float at(int i, int j) const {
+        if constexpr (PACKED) return j & 1 ? sm100::bf16hi(v[i][j / 2]) : sm100::bf16lo(v[i][j / 2]);
+        return __uint_as_float(v[i][j]);
+    }
+    // Magnitudes as integers that order like them: pairs of 16 bits (PACKED) or one of 32.
+    static __device__ __forceinline__ uint32_t mag(uint32_t w) { return w & (PACKED ? 0x7fff7fffu : 0x7fffffffu); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return PACKED ? __vmaxu2(a, b) : max(a, b); }
+    // The larger of a pair (PACKED), as the bits of a float.
+    static __device__ __forceinline__ uint32_t widest(uint32_t m) {
+        return PACKED ? max(m << 16, m & 0xffff0000u) : m;
+    }
+};
 
-// 128 x 128 blocks (SQUARE) or 128 x 1 column groups, written as it lies (SQUARE only) or
-// transposed through shared memory.
-template <typename T, bool VEC, bool SQUARE, bool TRANSPOSE>
-__global__ void __launch_bounds__(512) quantize_tile_kernel(const QuantParams p) {
+// 128 x 128 blocks (SQUARE), or 1 x 128 groups along the columns for q and along the rows for the
+// transpose.  ROWS writes q, TRANSPOSE the transpose, through shared memory.
+template <typename T, bool VEC, bool SQUARE, bool ROWS, bool TRANSPOSE>
+__global__ void __launch_bounds__(512, 2) quantize_tile_kernel(const QuantParams p) {
     using L = Tile<T, VEC>;
     constexpr int PITCH = 132;                   // bytes of a transposed column: 33 words, so columns meet other banks
-    __shared__ uint32_t cmax[16][128];
-    __shared__ float dv[128], iv[128];
+    constexpr int W = L::PACKED ? 64 : 128;      // words of a warp's column maxima
+    constexpr bool BY_COL = TRANSPOSE && !SQUARE;
+    __shared__ uint32_t cmax[BY_COL ? 16 : 1][BY_COL ? W + 2 : 16];
+    __shared__ float dv[BY_COL ? 128 : 1], iv[BY_COL ? 128 : 1];
     __shared__ uint32_t tq[TRANSPOSE ? 128 * PITCH / 4 : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t tc = (p.cols + 127) / 128;
     const int64_t br = blockIdx.x / tc, bc = blockIdx.x - br * tc;
     const int64_t r0 = br * 128, c0 = bc * 128;
-    float v[L::TR][L::TC];
-    load_tile<T, VEC>(p, r0, c0, warp, lane, v);
-    uint32_t m[L::TC];
-#pragma unroll
-    for (int j = 0; j < L::TC; ++j) {
-        m[j] = 0;
-#pragma unroll
-        for (int i = 0; i < L::TR; ++i) m[j] = max(m[j], magnitude(v[i][j]));
-    }
+    L t;
+    t.load(p, r0, c0, warp, lane);
     if constexpr (SQUARE) {
+        uint32_t m = 0;
 #pragma unroll
-        for (int j = 1; j < L::TC; ++j) m[0] = max(m[0], m[j]);
-        m[0] = __reduce_max_sync(0xffffffffu, m[0]);
-        if (lane == 0) cmax[warp][0] = m[0];
+        for (int i = 0; i < L::TR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = L::larger(m, L::mag(t.v[i][j]));
+        m = __reduce_max_sync(0xffffffffu, L::widest(m));
+        if (lane == 0) cmax[0][warp] = m;
         __syncthreads();
         if (warp == 0) {
-            const uint32_t a = __reduce_max_sync(0xffffffffu, lane < 16 ? cmax[lane][0] : 0u);
+            m = __reduce_max_sync(0xffffffffu, lane < 16 ? cmax[0][lane] : 0u);
             if (lane == 0) {
-                const float d = divisor(a);
+                const float d = divisor(m);
                 dv[0] = d;
                 iv[0] = __frcp_rn(d);
-                p.scale[(TRANSPOSE ? bc : br) * p.s_row + (TRANSPOSE ? br : bc) * p.s_grp] = __fdiv_rn(d, TOP);
+                if (ROWS) p.scale[br * p.s_row + bc * p.s_grp] = __fdiv_rn(d, TOP);
+                if (TRANSPOSE) p.scale_t[bc * p.st_row + br * p.st_grp] = __fdiv_rn(d, TOP);
             }
         }
-    } else {
-        if (L::LPR == 16) {
+        __syncthreads();
+    } else if constexpr (TRANSPOSE) {
+        uint32_t m[4];
 #pragma unroll
-            for (int j = 0; j < L::TC; ++j) m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        for (int j = 0; j < 4; ++j) {
+            m[j] = L::mag(t.v[0][j]);
+#pragma unroll
+            for (int i = 1; i < L::TR; ++i) m[j] = L::larger(m[j], L::mag(t.v[i][j]));
+            if (L::LPR == 16) m[j] = L::larger(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
         }
         if (L::LPR == 32 || lane < 16) {
 #pragma unroll
-            for (int j = 0; j < L::TC; ++j) cmax[warp][L::col(lane, j)] = m[j];
+            for (int j = 0; j < 4; ++j) cmax[warp][L::PACKED ? 4 * lane + j : L::col(lane, j)] = m[j];
         }
         __syncthreads();
-        if (threadIdx.x < 128) {
-            uint32_t a = 0;
+        // four threads a column, four warps' maxima each
+        const int c = threadIdx.x >> 2, part = threadIdx.x & 3;
+        uint32_t a = 0;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) a = max(a, cmax[k][threadIdx.x]);
+        for (int k = 0; k < 4; ++k) a = L::larger(a, cmax[4 * part + k][L::PACKED ? c >> 1 : c]);
+        a = L::larger(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = L::larger(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        if (L::PACKED) a = c & 1 ? a & 0xffff0000u : a << 16;
+        if (part == 0) {
             const float d = divisor(a);
-            dv[threadIdx.x] = d;
-            iv[threadIdx.x] = __frcp_rn(d);
-            if (c0 + threadIdx.x < p.cols) p.scale[(c0 + threadIdx.x) * p.s_row + br * p.s_grp] = __fdiv_rn(d, TOP);
+            dv[c] = d;
+            iv[c] = __frcp_rn(d);
+            if (c0 + c < p.cols) p.scale_t[(c0 + c) * p.st_row + br * p.st_grp] = __fdiv_rn(d, TOP);
         }
+        __syncthreads();
     }
-    __syncthreads();
     const int rr = L::row(warp, lane);
     if constexpr (TRANSPOSE) {
 #pragma unroll
@@ -553,7 +571,7 @@ __global__ void __launch_bounds__(512) quantize_tile_kernel(const QuantParams p)
             const float d = dv[SQUARE ? 0 : c], inv = iv[SQUARE ? 0 : c];
 #pragma unroll
             for (int i = 0; i < L::TR; i += 4) {
-                const float f[4] = {v[i][j], v[i + 1][j], v[i + 2][j], v[i + 3][j]};
+                const float f[4] = {t.at(i, j), t.at(i + 1, j), t.at(i + 2, j), t.at(i + 3, j)};
                 tq[c * (PITCH / 4) + (rr + i) / 4] = e4m3x4(f, d, inv);
             }
         }
@@ -564,7 +582,7 @@ __global__ void __launch_bounds__(512) quantize_tile_kernel(const QuantParams p)
         for (int k = 0; k < 8; ++k) {
             const int c = warp * 8 + k;
             if (c0 + c >= p.cols) break;
-            uint8_t* out = p.q + (c0 + c) * p.ldq + r;
+            uint8_t* out = p.qt + (c0 + c) * p.ldqt + r;
             const uint32_t b = tq[c * (PITCH / 4) + lane];
             if (r + 4 <= p.rows) {
                 *reinterpret_cast<uint32_t*>(out) = b;
@@ -573,23 +591,42 @@ __global__ void __launch_bounds__(512) quantize_tile_kernel(const QuantParams p)
                     if (r + e < p.rows) out[e] = (uint8_t)(b >> (8 * e));
             }
         }
-    } else {
-        const float d = dv[0], inv = iv[0];
+    }
+    if constexpr (ROWS) {
 #pragma unroll
         for (int i = 0; i < L::TR; ++i) {
             const int64_t r = r0 + rr + i;
-            if (r >= p.rows) break;
+            float d = SQUARE ? dv[0] : 0.f, inv = SQUARE ? iv[0] : 0.f;
+            if constexpr (!SQUARE) {             // the row's group: 16 or 32 lanes hold it
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = L::larger(m, L::mag(t.v[i][j]));
+                m = L::widest(m);
+                if (L::LPR == 32) {
+                    m = __reduce_max_sync(0xffffffffu, m);
+                } else {
+#pragma unroll
+                    for (int o = 8; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
+                d = divisor(m);
+                inv = __frcp_rn(d);
+                if (lane % L::LPR == 0 && r < p.rows) p.scale[r * p.s_row + bc * p.s_grp] = __fdiv_rn(d, TOP);
+            }
+            if (r >= p.rows) continue;
             uint8_t* out = p.q + r * p.ldq;
+            float f[L::TC];
+#pragma unroll
+            for (int j = 0; j < L::TC; ++j) f[j] = t.at(i, j);
             if constexpr (VEC) {
                 const int64_t c = c0 + L::col(lane, 0);
                 if (c < p.cols) {
                     if constexpr (L::TC == 8)
-                        *reinterpret_cast<uint2*>(out + c) = make_uint2(e4m3x4(v[i], d, inv), e4m3x4(v[i] + 4, d, inv));
+                        *reinterpret_cast<uint2*>(out + c) = make_uint2(e4m3x4(f, d, inv), e4m3x4(f + 4, d, inv));
                     else
-                        *reinterpret_cast<uint32_t*>(out + c) = e4m3x4(v[i], d, inv);
+                        *reinterpret_cast<uint32_t*>(out + c) = e4m3x4(f, d, inv);
                 }
             } else {
-                const uint32_t b = e4m3x4(v[i], d, inv);
+                const uint32_t b = e4m3x4(f, d, inv);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int64_t c = c0 + L::col(lane, j);

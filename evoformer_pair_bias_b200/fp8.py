@@ -22,20 +22,26 @@ from __future__ import annotations
 
 import torch
 
-from .attention import DTYPES, _check, _opt_f32, _ptr, _stream, load_library
+from .attention import DTYPES, EVO_OK, EvoError, _opt_f32, load_library
 
 GROUP = 128
 CODES = torch.float8_e4m3fn
+
+# A call costs the host some ten microseconds, as much as the smaller kernels take on the
+# GPU: the functions below avoid objects where a number will do (addresses and the raw
+# stream go to ctypes as integers) and ask each tensor once.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty = torch.empty_strided
 
 
 def _groups(n: int) -> int:
     return -(-n // GROUP)
 
 
-def _on(*tensors):
-    """Every tensor on one CUDA device, which is returned."""
-    dev = tensors[0].device
-    for t in tensors:
+def _on(first, *others):
+    """Every tensor (or None) on first's CUDA device, which is returned."""
+    dev = first.device
+    for t in others:
         if t is not None and t.device != dev:
             raise ValueError("all tensors must be on one device")
     if dev.type != "cuda":
@@ -43,15 +49,21 @@ def _on(*tensors):
     return dev
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _call(where, dev, *args):
     """One library call with `dev` current, on its current stream."""
     fn = getattr(load_library(), where)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(dev))
+    i = dev.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(dev))
-    _check(where, rc)
+        with torch.cuda.device(i):
+            rc = fn(*args, _raw_stream(i))
+    if rc != EVO_OK:
+        raise EvoError(where, rc)
 
 
 def _dtype(t, name):
@@ -61,43 +73,42 @@ def _dtype(t, name):
 
 
 def _rows(t):
-    """t [..., C] as (rows, C, 2-D view); a copy only where the leading axes do not fold into one."""
-    if t.dim() < 1:
+    """t [..., C] as (rows, C, matrix, row pitch); a copy only where the leading axes do not fold into one."""
+    shape = t.shape
+    if not shape:
         raise ValueError("expected at least one axis")
-    c = t.shape[-1]
-    if t.dim() == 2 and (t.stride(1) == 1 or c <= 1):
-        return t.shape[0], c, t
-    t2 = t.reshape(t.numel() // c if c else 0, c)
-    return t2.shape[0], c, t2 if c <= 1 or t2.stride(1) == 1 else t2.contiguous()
+    c = shape[-1]
+    t2 = t
+    if len(shape) != 2:
+        t2 = t.reshape(t.numel() // c if c else 0, c)
+    pitch, step = t2.stride()
+    if step != 1 and c > 1:
+        t2 = t2.contiguous()
+        pitch = c
+    return t2.shape[0], c, t2, pitch
 
 
 def empty_codes(rows: int, cols: int, device) -> torch.Tensor:
     """Uninitialised codes [rows, cols] whose rows start at multiples of 16 bytes."""
-    pitch = (cols + 15) // 16 * 16
-    return torch.empty_strided((rows, cols), (pitch, 1), dtype=CODES, device=device)
+    return _empty((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=CODES, device=device)
 
 
 def empty_scales(rows: int, groups: int, device) -> torch.Tensor:
     """Uninitialised scales [rows, groups], laid out group by group (the rows of a group contiguous)."""
-    return torch.empty_strided((rows, groups), (1, max(rows, 1)), dtype=torch.float32, device=device)
-
-
-def _scale_strides(s):
-    return max(s.stride(0), 1), max(s.stride(1), 1)
-
-
-def _check_dense(t, shape, dtype, name, dev):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or \
-            (t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} with a contiguous last axis")
+    return _empty((rows, groups), (1, rows or 1), dtype=torch.float32, device=device)
 
 
 def _weight(weight, cols):
     if weight is None:
         return 0
-    if weight.dim() != 1 or weight.shape[0] != cols or not weight.is_contiguous():
+    if weight.shape != (cols,) or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous [{cols}] tensor")
     return _dtype(weight, "weight")
+
+
+def _lead(t, lead):
+    """A result [rows, ...] with the leading axes of its input."""
+    return t.unflatten(0, lead) if lead else t[0]
 
 
 def add_rms_norm_fp8(x, residual=None, weight=None, eps=1e-6, want_n=False):
@@ -109,56 +120,63 @@ def add_rms_norm_fp8(x, residual=None, weight=None, eps=1e-6, want_n=False):
     ``want_n=True`` returns n, rounded to x's type, as a fifth value.
     """
     dev = _on(x, residual, weight)
+    dtype, shape = x.dtype, x.shape
     dt = _dtype(x, "x")
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
-        raise ValueError("residual must have x's shape and dtype")
-    rows, c, x2 = _rows(x)
+    rows, c, x2, ldx = _rows(x)
     wd = _weight(weight, c)
-    r2 = None if residual is None else _rows(residual)[2]
-    lead = x.shape[:-1]
-    q, scale = empty_codes(rows, c, dev), empty_scales(rows, _groups(c), dev)
-    h = None if residual is None else torch.empty((rows, c), dtype=x.dtype, device=dev)
-    n = torch.empty((rows, c), dtype=x.dtype, device=dev) if want_n else None
-    rstd = torch.empty(lead, dtype=torch.float32, device=dev)
-    sr, sg = _scale_strides(scale)
-    _call("evo_add_rms_norm_fp8", dev, rows, c, dt, _ptr(x2), x2.stride(0), _ptr(r2),
-          0 if r2 is None else r2.stride(0), _ptr(weight), wd, float(eps), _ptr(q), q.stride(0), _ptr(scale), sr, sg,
-          _ptr(h), c, _ptr(n), c, _ptr(rstd))
-    if x.dim() != 2:
-        q, scale = q.unflatten(0, lead) if lead else q[0], scale.unflatten(0, lead) if lead else scale[0]
-    out = (q, scale, x if h is None else h.view(x.shape), rstd)
-    return out + (n.view(x.shape),) if want_n else out
+    q, scale = empty_codes(rows, c, dev), empty_scales(rows, -(-c // GROUP), dev)
+    r2 = h = n = None
+    ldr = 0
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != dtype:
+            raise ValueError("residual must have x's shape and dtype")
+        r2, ldr = _rows(residual)[2:]
+        h = _empty((rows, c), (c, 1), dtype=dtype, device=dev)
+    if want_n:
+        n = _empty((rows, c), (c, 1), dtype=dtype, device=dev)
+    rstd = _empty((rows,), (1,), dtype=torch.float32, device=dev)
+    _call("evo_add_rms_norm_fp8", dev, rows, c, dt, x2.data_ptr(), ldx, _addr(r2), ldr, _addr(weight), wd, eps,
+          q.data_ptr(), (c + 15) // 16 * 16, scale.data_ptr(), 1, rows or 1, _addr(h), c, _addr(n), c, rstd.data_ptr())
+    if h is None:
+        h = x
+    if len(shape) != 2:
+        lead = shape[:-1]
+        q, scale, rstd = _lead(q, lead), _lead(scale, lead), _lead(rstd, lead)
+        h = h.view(shape) if residual is not None else h
+        n = n.view(shape) if want_n else None
+    return (q, scale, h, rstd, n) if want_n else (q, scale, h, rstd)
 
 
-def add_rms_norm_bwd(dy, dh, h, rstd, weight=None, want_dweight=True):
+def add_rms_norm_bwd(dy, dh, h, rstd, weight=None, want_dweight=True, dweight_dtype=torch.float32):
     """Gradients of add_rms_norm_fp8 with its rounding to 8 bits passed over: ``(dx, dweight)``.
 
     dy: gradient with respect to n; dh: the one that reaches h by the residual stream, or None;
-    h, rstd: the forward's.  dx (h's type) is the gradient of x and of residual alike; dweight is
-    fp32 ``[C]`` (None with ``want_dweight=False``).
+    h, rstd: the forward's.  dx (h's type) is the gradient of x and of residual alike; dweight
+    ``[C]`` is summed in fp32 and fp32 or, with ``dweight_dtype``, bf16 (None with ``want_dweight=False``).
     """
-    dev = _on(dy, dh, h, rstd, weight)
+    dev = _on(h, dy, dh, rstd, weight)
+    dtype, shape = h.dtype, h.shape
     dt = _dtype(h, "h")
-    for name, t in (("dy", dy), ("dh", dh)):
-        if t is not None and (t.shape != h.shape or t.dtype != h.dtype):
-            raise ValueError(f"{name} must have h's shape and dtype")
-    rows, c, h2 = _rows(h)
-    if rstd.dtype != torch.float32 or rstd.shape != h.shape[:-1] or not rstd.is_contiguous():
-        raise ValueError(f"rstd must be a contiguous fp32 tensor of shape {tuple(h.shape[:-1])}")
+    rows, c, h2, ldh = _rows(h)
+    if dy.shape != shape or dy.dtype != dtype or (dh is not None and (dh.shape != shape or dh.dtype != dtype)):
+        raise ValueError("dy and dh must have h's shape and dtype")
+    if rstd.dtype != torch.float32 or rstd.shape != shape[:-1] or not rstd.is_contiguous():
+        raise ValueError(f"rstd must be a contiguous fp32 tensor of shape {tuple(shape[:-1])}")
+    if dweight_dtype not in DTYPES:
+        raise ValueError(f"dweight_dtype must be bf16 or fp32, got {dweight_dtype}")
     wd = _weight(weight, c)
-    dy2 = _rows(dy)[2]
-    dh2 = None if dh is None else _rows(dh)[2]
-    dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    dy2, lddy = _rows(dy)[2:]
+    dh2, lddh = (None, 0) if dh is None else _rows(dh)[2:]
+    dx = _empty((rows, c), (c, 1), dtype=dtype, device=dev)
     dweight = ws = None
     nbytes = 0
     if want_dweight:
-        dweight = torch.empty(c, dtype=torch.float32, device=dev)
-        nbytes = int(load_library().evo_add_rms_norm_bwd_workspace_bytes(rows, c))
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    _call("evo_add_rms_norm_bwd", dev, rows, c, dt, _ptr(dy2), dy2.stride(0), _ptr(dh2),
-          0 if dh2 is None else dh2.stride(0), _ptr(h2), h2.stride(0), _ptr(rstd), _ptr(weight), wd, _ptr(dx), c,
-          _ptr(dweight), _ptr(ws), nbytes)
-    return dx, dweight
+        dweight = _empty((c,), (1,), dtype=dweight_dtype, device=dev)
+        nbytes = load_library().evo_add_rms_norm_bwd_workspace_bytes(rows, c)
+        ws = _empty((nbytes // 4,), (1,), dtype=torch.float32, device=dev)
+    _call("evo_add_rms_norm_bwd", dev, rows, c, dt, dy2.data_ptr(), lddy, _addr(dh2), lddh, h2.data_ptr(), ldh,
+          rstd.data_ptr(), _addr(weight), wd, dx.data_ptr(), c, _addr(dweight), DTYPES[dweight_dtype], _addr(ws), nbytes)
+    return dx if len(shape) == 2 else dx.view(shape), dweight
 
 
 def quantize_fp8(x, square=False, transpose=False):
@@ -170,39 +188,73 @@ def quantize_fp8(x, square=False, transpose=False):
     """
     dev = _on(x)
     dt = _dtype(x, "x")
-    if square and x.dim() != 2:
+    shape = x.shape
+    if square and len(shape) != 2:
         raise ValueError("square blocks are of a matrix [R, C]")
-    rows, c, x2 = _rows(x)
+    rows, c, x2, ldx = _rows(x)
     qr, qc = (c, rows) if transpose else (rows, c)
+    g = -(-qc // GROUP)
     q = empty_codes(qr, qc, dev)
     if square:
-        scale = torch.empty((_groups(qr), _groups(qc)), dtype=torch.float32, device=dev)
+        scale = _empty((-(-qr // GROUP), g), (g or 1, 1), dtype=torch.float32, device=dev)
+        sr, sg = g or 1, 1
     else:
-        scale = empty_scales(qr, _groups(qc), dev)
-    sr, sg = _scale_strides(scale)
-    _call("evo_quantize_fp8", dev, rows, c, dt, _ptr(x2), x2.stride(0), int(square), int(transpose), _ptr(q),
-          q.stride(0), _ptr(scale), sr, sg)
-    if not transpose and x.dim() != 2:
-        lead = x.shape[:-1]
-        q, scale = (q.unflatten(0, lead), scale.unflatten(0, lead)) if lead else (q[0], scale[0])
+        scale = empty_scales(qr, g, dev)
+        sr, sg = 1, qr or 1
+    _call("evo_quantize_fp8", dev, rows, c, dt, x2.data_ptr(), ldx, bool(square), bool(transpose), q.data_ptr(),
+          (qc + 15) // 16 * 16, scale.data_ptr(), sr, sg)
+    if not transpose and len(shape) != 2:
+        q, scale = _lead(q, shape[:-1]), _lead(scale, shape[:-1])
     return q, scale
 
 
+def quantize_fp8_both(x, square=False):
+    """quantize_fp8 of x and of x.T in one pass over x: ``(q, scale, q_t, scale_t)``.
+
+    For training: a weight's blocks serve its product and, transposed, the input's gradient; an output
+    gradient's groups along both axes serve the input's and the weight's gradient.  With
+    ``square=True`` the two hold the same values, transposed.
+    """
+    dev = _on(x)
+    dt = _dtype(x, "x")
+    shape = x.shape
+    if square and len(shape) != 2:
+        raise ValueError("square blocks are of a matrix [R, C]")
+    rows, c, x2, ldx = _rows(x)
+    gr, gc = -(-rows // GROUP), -(-c // GROUP)
+    q, qt = empty_codes(rows, c, dev), empty_codes(c, rows, dev)
+    if square:
+        scale = _empty((gr, gc), (gc or 1, 1), dtype=torch.float32, device=dev)
+        scale_t = scale.t()
+        strides = gc or 1, 1, 1, gc or 1
+    else:
+        scale, scale_t = empty_scales(rows, gc, dev), empty_scales(c, gr, dev)
+        strides = 1, rows or 1, 1, c or 1
+    _call("evo_quantize_fp8_both", dev, rows, c, dt, x2.data_ptr(), ldx, bool(square), q.data_ptr(),
+          (c + 15) // 16 * 16, scale.data_ptr(), strides[0], strides[1], qt.data_ptr(), (rows + 15) // 16 * 16,
+          scale_t.data_ptr(), strides[2], strides[3])
+    if len(shape) != 2:
+        q, scale = _lead(q, shape[:-1]), _lead(scale, shape[:-1])
+    return q, scale, qt, scale_t
+
+
 def _codes(t, name):
-    """Codes [..., C] as a matrix, without a copy."""
+    """Codes [..., C] as (rows, C, address, pitch), without a copy."""
     if t.dtype != CODES:
         raise ValueError(f"{name} must hold {CODES} codes, got {t.dtype}")
-    if t.dim() == 2:
-        t2 = t
-    else:
-        t2 = t.view(-1, t.shape[-1]) if t.is_contiguous() else t.flatten(0, -2) if t.dim() > 1 else t[None]
-        if t2.data_ptr() != t.data_ptr():
+    if t.dim() != 2:
+        flat = t[None] if t.dim() == 1 else t.flatten(0, -2)
+        if flat.numel() and flat.data_ptr() != t.data_ptr():
             raise ValueError(f"{name}: the leading axes must fold into one without a copy")
-    if t2.shape[1] > 1 and t2.stride(1) != 1:
+        t = flat
+    rows, c = t.shape
+    pitch, step = t.stride()
+    at = t.data_ptr()
+    if step != 1 and c > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    if (t2.shape[0] > 1 and t2.stride(0) % 16) or t2.data_ptr() % 16:
+    if at % 16 or (rows > 1 and pitch % 16):
         raise ValueError(f"{name}: rows must start at multiples of 16 bytes (see empty_codes)")
-    return t2
+    return rows, c, at, pitch
 
 
 def fp8_linear(xq, x_scale, wq, w_scale, bias=None, out_dtype=torch.bfloat16):
@@ -216,35 +268,27 @@ def fp8_linear(xq, x_scale, wq, w_scale, bias=None, out_dtype=torch.bfloat16):
     dev = _on(xq, x_scale, wq, w_scale, bias)
     if out_dtype not in DTYPES:
         raise ValueError(f"out_dtype must be bf16 or fp32, got {out_dtype}")
-    x2, w2 = _codes(xq, "xq"), _codes(wq, "wq")
-    M, K = x2.shape
-    N = w2.shape[0]
-    G = _groups(K)
-    if wq.dim() != 2 or w2.shape[1] != K:
+    M, K, x_at, ldx = _codes(xq, "xq")
+    N, wk, w_at, ldw = _codes(wq, "wq")
+    if wq.dim() != 2 or wk != K:
         raise ValueError(f"wq must be [N, {K}], got {tuple(wq.shape)}")
-    if tuple(x_scale.shape) != tuple(xq.shape[:-1]) + (G,) or x_scale.dtype != torch.float32:
-        raise ValueError(f"x_scale must be fp32 of shape {tuple(xq.shape[:-1]) + (G,)}")
-    if w_scale.dtype != torch.float32 or w_scale.dim() != 2 or w_scale.shape[1] != G or \
-            w_scale.shape[0] not in (N, _groups(N)):
-        raise ValueError(f"w_scale must be fp32 of shape [{_groups(N)}, {G}] (blocks) or [{N}, {G}] (rows)")
-    w_rows = w_scale.shape[0] != _groups(N)
-    xs = x_scale if x_scale.dim() == 2 else x_scale.reshape(M, G)
-    y = torch.empty(xq.shape[:-1] + (N,), dtype=out_dtype, device=dev)
-    b = _opt_f32(bias, N, dev)
-    _call("evo_fp8_linear", dev, M, N, K, _ptr(x2), x2.stride(0), _ptr(xs), xs.stride(0), xs.stride(1), _ptr(w2),
-          w2.stride(0), _ptr(w_scale), w_scale.stride(0), w_scale.stride(1), int(w_rows), _ptr(b), DTYPES[out_dtype],
-          _ptr(y), N)
-    return y
-
-
-def _input_grad(dy, w):
-    """dy @ w in 8 bits: dy [..., N] in 1 x 128 groups, the transposed w [N, K] in blocks."""
-    return fp8_linear(*quantize_fp8(dy), *quantize_fp8(w, square=True, transpose=True), out_dtype=dy.dtype)
-
-
-def _weight_grad(dy, x, dtype):
-    """dy^T @ x in 8 bits, both in groups of 128 rows."""
-    return fp8_linear(*quantize_fp8(dy, transpose=True), *quantize_fp8(x, transpose=True), out_dtype=dtype)
+    G = -(-K // GROUP)
+    lead = xq.shape[:-1]
+    if x_scale.shape != (*lead, G) or x_scale.dtype != torch.float32:
+        raise ValueError(f"x_scale must be fp32 of shape {(*lead, G)}")
+    sn = w_scale.shape[0] if w_scale.dim() == 2 and w_scale.shape[1] == G else -1
+    blocks = -(-N // GROUP)
+    if w_scale.dtype != torch.float32 or sn not in (N, blocks):
+        raise ValueError(f"w_scale must be fp32 of shape [{blocks}, {G}] (blocks) or [{N}, {G}] (rows)")
+    xs = x_scale if len(lead) == 1 else x_scale.reshape(M, G)
+    sxr, sxg = xs.stride()
+    swr, swg = w_scale.stride()
+    y = _empty((M, N), (N, 1), dtype=out_dtype, device=dev)
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
+        bias = _opt_f32(bias, N, dev)
+    _call("evo_fp8_linear", dev, M, N, K, x_at, ldx, xs.data_ptr(), sxr, sxg, w_at, ldw, w_scale.data_ptr(), swr, swg,
+          sn != blocks, _addr(bias), DTYPES[out_dtype], y.data_ptr(), N)
+    return y if len(lead) == 1 else y.view(*lead, N)
 
 
 def _training_weight(x, w):
@@ -253,21 +297,49 @@ def _training_weight(x, w):
     _dtype(w, "w")
 
 
+def _forward(ctx, q, scale, w, dtype):
+    """q @ w.T; keeps on ctx what the input's gradient wants of w, quantised in the same pass."""
+    if ctx.needs_input_grad[0] or any(ctx.needs_input_grad[1:-1]):
+        wq, ws, wqt, wst = quantize_fp8_both(w, square=True)
+    else:
+        (wq, ws), wqt, wst = quantize_fp8(w, square=True), None, None
+    return fp8_linear(q, scale, wq, ws, out_dtype=dtype), wqt, wst
+
+
+def _gradients(dy, wqt, wst, x, w_dtype, want_dx, want_dw):
+    """(dy @ w, dy^T @ x) in 8 bits: groups of 128 outputs, and of 128 rows."""
+    dx = dw = None
+    if want_dw and dy.numel() == 0:              # the empty sum
+        dw = torch.zeros((dy.shape[-1], x.shape[-1]), dtype=w_dtype, device=dy.device)
+        want_dw = False
+    if want_dx and want_dw:
+        q, s, qt, st = quantize_fp8_both(dy)
+    elif want_dx:
+        q, s = quantize_fp8(dy)
+    elif want_dw:
+        qt, st = quantize_fp8(dy, transpose=True)
+    if want_dx:
+        dx = fp8_linear(q, s, wqt, wst, out_dtype=dy.dtype)
+    if want_dw:
+        dw = fp8_linear(qt, st, *quantize_fp8(x, transpose=True), out_dtype=w_dtype)
+    return dx, dw
+
+
 class Fp8Linear(torch.autograd.Function):
     """y = x @ w.T in 8 bits, both directions (x: bf16 or fp32; y in x's type; w [N, K])."""
 
     @staticmethod
     def forward(ctx, x, w):
         _training_weight(x, w)
-        ctx.save_for_backward(x, w)
-        return fp8_linear(*quantize_fp8(x), *quantize_fp8(w, square=True), out_dtype=x.dtype)
+        y, wqt, wst = _forward(ctx, *quantize_fp8(x), w, x.dtype)
+        ctx.save_for_backward(x, wqt, wst)
+        ctx.w_dtype = w.dtype
+        return y
 
     @staticmethod
     def backward(ctx, dy):
-        x, w = ctx.saved_tensors
-        dx = _input_grad(dy, w) if ctx.needs_input_grad[0] else None
-        dw = _weight_grad(dy, x, w.dtype) if ctx.needs_input_grad[1] else None
-        return dx, dw
+        x, wqt, wst = ctx.saved_tensors
+        return _gradients(dy, wqt, wst, x, ctx.w_dtype, *ctx.needs_input_grad)
 
 
 class AddRmsNormLinear(torch.autograd.Function):
@@ -276,26 +348,27 @@ class AddRmsNormLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, w):
         _training_weight(x, w)
-        q, scale, h, rstd, n = add_rms_norm_fp8(x, residual, weight, eps, want_n=True)
-        y = fp8_linear(q, scale, *quantize_fp8(w, square=True), out_dtype=x.dtype)
+        q, scale, h, rstd, *n = add_rms_norm_fp8(x, residual, weight, eps, want_n=ctx.needs_input_grad[4])
+        y, wqt, wst = _forward(ctx, q, scale, w, x.dtype)
         if residual is None:
             h = x.view_as(x)
         ctx.set_materialize_grads(False)         # an unused output costs nothing
-        ctx.save_for_backward(h, rstd, n, weight, w)
+        ctx.save_for_backward(h, rstd, n[0] if n else None, weight, wqt, wst)
+        ctx.w_dtype = w.dtype
         return h, y
 
     @staticmethod
     def backward(ctx, dh, dy):
-        h, rstd, n, weight, w = ctx.saved_tensors
+        h, rstd, n, weight, wqt, wst = ctx.saved_tensors
+        for_x, for_res, for_weight, _, for_w = ctx.needs_input_grad
         if dy is None:
-            return dh if ctx.needs_input_grad[0] else None, dh if ctx.needs_input_grad[1] else None, None, None, None
-        dw = _weight_grad(dy, n, w.dtype) if ctx.needs_input_grad[4] else None
+            return dh if for_x else None, dh if for_res else None, None, None, None
+        dn, dw = _gradients(dy, wqt, wst, n, ctx.w_dtype, for_x or for_res or for_weight, for_w)
         dx = dweight = None
-        if any(ctx.needs_input_grad[:3]):
-            want = weight is not None and ctx.needs_input_grad[2]
-            dx, dweight = add_rms_norm_bwd(_input_grad(dy, w), dh, h, rstd, weight, want_dweight=want)
-            dweight = dweight.to(weight.dtype) if want else None
-        return (dx if ctx.needs_input_grad[0] else None, dx if ctx.needs_input_grad[1] else None, dweight, None, dw)
+        if dn is not None:
+            dx, dweight = add_rms_norm_bwd(dn, dh, h, rstd, weight, for_weight,
+                                           weight.dtype if for_weight else torch.float32)
+        return dx if for_x else None, dx if for_res else None, dweight, None, dw
 
 
 def fp8_linear_train(x, w):

@@ -362,9 +362,10 @@ evo_status_t evo_add_rms_norm_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype,
  *   dx[r,:] = dh[r,:] + rstd[r] * (g - n' * mean_c(g * n'))
  *   dweight[c] = sum_r dy[r,c] * n'[r,c]
  *
- * dx (of dtype) is the gradient of x and of residual alike.  dweight: fp32
- * [cols], or NULL (not computed, no workspace needed).  The sum over rows has
- * a fixed order and no atomics: the same bits on every run.  workspace:
+ * dx (of dtype) is the gradient of x and of residual alike.  dweight: [cols]
+ * of dw_dtype (rounded once, from an fp32 sum), or NULL (not computed, no
+ * workspace needed).  The sum over rows has a fixed order and no atomics: the
+ * same bits on every run.  workspace:
  * evo_add_rms_norm_bwd_workspace_bytes(rows, cols) bytes, 16-byte aligned,
  * contents arbitrary; calls that may overlap need one each.  rows == 0 sets
  * dweight to zero.
@@ -372,8 +373,8 @@ evo_status_t evo_add_rms_norm_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype,
 size_t evo_add_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 evo_status_t evo_add_rms_norm_bwd(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* dy, int64_t lddy,
                                   const void* dh, int64_t lddh, const void* h, int64_t ldh, const float* rstd,
-                                  const void* weight, evo_dtype_t w_dtype, void* dx, int64_t lddx, float* dweight,
-                                  void* workspace, size_t workspace_bytes, void* stream);
+                                  const void* weight, evo_dtype_t w_dtype, void* dx, int64_t lddx, void* dweight,
+                                  evo_dtype_t dw_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * A matrix x [rows, cols] of `dtype` (row pitch ldx, elements) in e4m3.
@@ -387,6 +388,18 @@ evo_status_t evo_add_rms_norm_bwd(int64_t rows, int64_t cols, evo_dtype_t dtype,
 evo_status_t evo_quantize_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx, int square,
                               int transpose, void* q, int64_t ldq, float* scale, int64_t scale_row,
                               int64_t scale_group, void* stream);
+
+/*
+ * Both at once, x read once: q [rows, cols] and q_t = its transpose [cols,
+ * rows], each with its scales as above.  square == 0: q in 1 x 128 groups
+ * along the columns of x, q_t in groups along its rows (two roundings of x).
+ * square != 0: the same codes and scales, transposed; scale_t may be scale
+ * with the strides exchanged (both are written with the same values).
+ */
+evo_status_t evo_quantize_fp8_both(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx,
+                                   int square, void* q, int64_t ldq, float* scale, int64_t scale_row,
+                                   int64_t scale_group, void* q_t, int64_t ldq_t, float* scale_t,
+                                   int64_t scale_t_row, int64_t scale_t_group, void* stream);
 
 /*
  * y = x @ w^T + bias of two 8-bit matrices x [M, K] and w [N, K]:

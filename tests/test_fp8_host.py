@@ -56,6 +56,16 @@ def test_quantize_refusals(lib):
     assert f(1 << 40, 1 << 20, 0, FAKE, 1 << 20, 1, 0, FAKE, 1 << 20, FAKE, 1, 8, NUL) == 2   # more blocks than a grid
 
 
+def test_quantize_both_refusals(lib):
+    def f(rows=8, cols=8, dtype=0, x=FAKE, ldx=8, q=FAKE, ldq=16, s=FAKE, sr=1, qt=FAKE, ldqt=16, st=FAKE, stg=8):
+        return lib.evo_quantize_fp8_both(rows, cols, dtype, x, ldx, 0, q, ldq, s, sr, 8, qt, ldqt, st, 1, stg, NUL)
+    assert f(rows=0, x=NUL, q=NUL) == 0 and f(cols=0, x=NUL, qt=NUL) == 0
+    assert f(rows=-1) == 1 and f(dtype=4) == 1 and f(x=NUL) == 1 and f(ldx=-8) == 1
+    assert f(q=NUL) == 1 and f(qt=NUL) == 1 and f(s=NUL) == 1 and f(st=NUL) == 1 and f(sr=0) == 1 and f(stg=0) == 1
+    assert f(cols=32, ldx=32, ldq=16) == 1 and f(rows=32, ldqt=16) == 1
+    assert f(ldq=24) == 2 and f(ldqt=24) == 2 and f(q=ODD4) == 2 and f(qt=ODD4) == 2
+
+
 def test_norm_refusals(lib):
     def f(rows=8, cols=64, dtype=0, x=FAKE, ldx=64, res=NUL, ldr=0, w=NUL, wd=0, eps=1e-5, q=FAKE, ldq=64, s=FAKE, sr=1,
           sg=8, h=NUL, ldh=0, n=NUL, ldn=0, rstd=NUL):
@@ -72,10 +82,12 @@ def test_norm_refusals(lib):
 
 def test_norm_bwd_refusals_and_workspace(lib):
     def f(rows=8, cols=64, dtype=0, dy=FAKE, dh=NUL, h=FAKE, rstd=FAKE, w=NUL, wd=0, dx=FAKE, lddx=64, dw=NUL, ws=NUL,
-          nb=0):
-        return lib.evo_add_rms_norm_bwd(rows, cols, dtype, dy, 64, dh, 64, h, 64, rstd, w, wd, dx, lddx, dw, ws, nb, NUL)
+          nb=0, dwd=1):
+        return lib.evo_add_rms_norm_bwd(rows, cols, dtype, dy, 64, dh, 64, h, 64, rstd, w, wd, dx, lddx, dw, dwd, ws, nb,
+                                        NUL)
     assert f(rows=0, dy=NUL, h=NUL, rstd=NUL, dx=NUL) == 0
     assert f(rows=-1) == 1 and f(cols=0) == 1 and f(dtype=2) == 1 and f(wd=2) == 1
+    assert f(dwd=9) == 1 and f(dw=ODD, ws=FAKE, nb=1 << 30) == 1
     assert f(dy=NUL) == 1 and f(h=NUL) == 1 and f(rstd=NUL) == 1 and f(dx=NUL) == 1 and f(lddx=8) == 1
     assert f(cols=40000, lddx=40000) == 2
     assert f(dw=FAKE) == 3 and f(dw=FAKE, ws=FAKE, nb=255) == 3
@@ -106,7 +118,7 @@ def test_binding_refusals():
     c = torch.zeros((4, 64), dtype=torch.uint8).view(fp8.CODES)
     with pytest.raises(ValueError, match="codes"):
         fp8._codes(x, "xq")
-    assert fp8._codes(c, "xq").shape == (4, 64)
+    assert fp8._codes(c, "xq") == (4, 64, c.data_ptr(), 64)
     with pytest.raises(ValueError, match="multiples of 16"):
         fp8._codes(torch.zeros((4, 60), dtype=torch.uint8).view(fp8.CODES), "xq")
     with pytest.raises(ValueError, match="contiguous"):
@@ -124,10 +136,10 @@ def test_binding_refusals():
 
 def test_rows_folds_leading_axes_without_a_copy_where_it_can():
     x = torch.zeros((2, 3, 4, 8))
-    r, c, v = fp8._rows(x)
-    assert (r, c) == (24, 8) and v.data_ptr() == x.data_ptr()
-    r, c, v = fp8._rows(x[..., 2:6])
-    assert (r, c) == (24, 4) and v.stride(0) == 8 and v.data_ptr() == x.data_ptr() + 8
-    r, c, v = fp8._rows(x.transpose(0, 3))                   # no contiguous last axis: copied
-    assert (r, c) == (8 * 3 * 4, 2) and v.stride(1) == 1
+    r, c, v, ld = fp8._rows(x)
+    assert (r, c, ld) == (24, 8, 8) and v.data_ptr() == x.data_ptr()
+    r, c, v, ld = fp8._rows(x[..., 2:6])
+    assert (r, c, ld) == (24, 4, 8) and v.data_ptr() == x.data_ptr() + 8
+    r, c, v, ld = fp8._rows(x.transpose(0, 3))               # no contiguous last axis: copied
+    assert (r, c, ld) == (8 * 3 * 4, 2, 2) and v.stride(1) == 1
     assert fp8._rows(torch.zeros(0, 8))[0] == 0 and fp8._rows(torch.zeros(8))[0] == 1

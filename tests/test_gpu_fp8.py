@@ -83,6 +83,18 @@ def test_quantize(rows, cols, square, transpose, dtype):
     close(scale, m / 448, 2.0 ** -23)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("square", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (128, 128), (129, 127), (300, 512), (257, 1001), (5, 2048)])
+def test_quantize_both_is_the_two_calls(rows, cols, square, dtype):
+    x = stream_rows(rows, cols, gen(rows + cols), dtype)
+    q, s, qt, st = fp8.quantize_fp8_both(x, square=square)
+    for got, want in (((q, s), fp8.quantize_fp8(x, square=square)), ((qt, st), fp8.quantize_fp8(x, square=square, transpose=True))):
+        assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+    if square:
+        assert torch.equal(q.view(torch.uint8).t(), qt.view(torch.uint8)) and torch.equal(s.t(), st)
+
+
 def test_quantize_breaks_ties_to_even():
     # 448 * v / m is a border for many bf16 pairs (448 = 7 * 64): v = 3 m / 2^k, 21 k / m ...
     m = torch.arange(128, 256, device="cuda", dtype=F32)[:, None]
@@ -271,6 +283,7 @@ def test_add_rms_norm_bwd(rows, cols, stream, dtype, wdtype):
     dx2, none = fp8.add_rms_norm_bwd(dy, dh, h, rstd, w, want_dweight=False)
     assert none is None and torch.equal(dx, dx2)
     assert torch.equal(fp8.add_rms_norm_bwd(dy, dh, h, rstd, w)[1], dw)
+    assert torch.equal(fp8.add_rms_norm_bwd(dy, dh, h, rstd, w, dweight_dtype=BF16)[1], dw.to(BF16))
 
 
 def test_add_rms_norm_bwd_against_differences():
@@ -434,7 +447,7 @@ def test_norm_projection_attention_projection_norm():
 
 # ------------------------------------------------------------------- training
 def rel(a, b):
-    return float((a.double() - b).norm() / b.norm())
+    return float((a.detach().double() - b).norm() / b.norm())
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -503,6 +516,24 @@ def test_training_functions_with_unused_outputs_and_expanded_gradients():
     assert torch.equal(gx, torch.ones_like(gx))
     gx, gr = torch.autograd.grad(y.sum(), (x2, r2))
     assert torch.equal(gx, gr) and torch.isfinite(gx).all()
+    e = torch.zeros((0, 128), dtype=BF16, device="cuda", requires_grad=True)
+    ge, gw = torch.autograd.grad(fp8.fp8_linear_train(e, w).sum(), (e, w))
+    assert ge.shape == (0, 128) and (gw == 0).all()
+    h, y = fp8.add_rms_norm_linear(e, e, None, 1e-5, w)
+    ge, gw = torch.autograd.grad((h.sum() + y.sum()), (e, w))
+    assert ge.shape == (0, 128) and (gw == 0).all()
+
+
+def test_gradients_use_the_weight_of_the_forward():
+    g = gen(68)
+    x, w = randn((40, 128), g, BF16).requires_grad_(True), randn((64, 128), g, BF16).requires_grad_(True)
+    dy = randn((40, 64), g, BF16)
+    (want,) = torch.autograd.grad(fp8.fp8_linear_train(x, w), x, dy)
+    y = fp8.fp8_linear_train(x, w)
+    with torch.no_grad():
+        w.mul_(3)
+    (got,) = torch.autograd.grad(y, x, dy)
+    assert torch.equal(got, want)
 
 
 # ------------------------------------------------------------------- streams and graphs
