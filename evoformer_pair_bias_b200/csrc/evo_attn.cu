@@ -373,66 +373,77 @@ bool rows_vec(const void* ptr, int64_t rows, int64_t cols, int64_t ld, int64_t e
     return rows_vec(ptr, cols, rows > 1 ? ld : 0, e);
 }
 
-// How a row is held by warps of 256 columns: nv fragments in each of wpr warps.
+// How a row is held: nv fragments of 256 columns in each of wpr warps, and the threads of a block.
 struct RowSplit {
-    int nv, wpr, warps;          // warps per block
+    int nv, wpr, threads;
 };
 constexpr int64_t kMaxRowCols = 32768;
+// Forward: blocks of up to 8 warps, as many rows in them as fit; more fragments per warp for wider
+// rows.  Above 8192 columns up to 32 warps of four.
 RowSplit row_split(int64_t cols) {
-    RowSplit s{1, 1, 8};
-    while ((int64_t)s.wpr * 256 < cols && s.wpr < 32) s.wpr *= 2;
-    while ((int64_t)s.nv * s.wpr * 256 < cols) s.nv *= 2;
-    s.warps = std::max(8, s.wpr);
-    return s;
+    const int chunks = (int)((cols + 255) / 256);
+    const int nv = chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4, wpr = (chunks + nv - 1) / nv;
+    return {nv, wpr, 32 * (wpr <= 8 ? 8 / wpr * wpr : wpr)};
+}
+// Backward: twice the values per column, so one fragment per warp up to 20 warps (102 registers
+// each), two up to 40 chunks.
+RowSplit row_split_bwd(int64_t cols) {
+    const int chunks = (int)((cols + 255) / 256);
+    const int nv = chunks <= 20 ? 1 : chunks <= 40 ? 2 : 4, wpr = (chunks + nv - 1) / nv;
+    return {nv, wpr, 32 * (wpr <= 8 ? 8 / wpr * wpr : wpr)};
 }
 
-template <template <typename, bool, int> class L, typename P>
-void by_layout(evo_dtype_t dtype, bool vec, int nv, const P& p) {
-    auto pick = [&](auto t, auto v) {
-        using T = decltype(t);
-        constexpr bool V = decltype(v)::value;
-        switch (nv) {
-            case 1: L<T, V, 1>::launch(p); break;
-            case 2: L<T, V, 2>::launch(p); break;
-            default: L<T, V, 4>::launch(p); break;
-        }
-    };
-    auto with = [&](auto t) { vec ? pick(t, std::true_type{}) : pick(t, std::false_type{}); };
+// Blocks for `rows` of which a block takes `per` at a time: at most what runs at once.
+template <typename K>
+int walking_grid(K kernel, int threads, int64_t rows, int64_t per) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+    return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * n);
+}
+
+// f(T{}, VEC) with the call's type and alignment as types.
+template <typename F>
+void by_type(evo_dtype_t dtype, bool vec, F f) {
+    auto with = [&](auto t) { vec ? f(t, std::true_type{}) : f(t, std::false_type{}); };
     dtype == EVO_DTYPE_BF16 ? with(__nv_bfloat16{}) : with(float{});
 }
 
-struct NormLaunch {
-    evo::fp8::NormParams p;
-    RowSplit s;
-    int grid;
-    cudaStream_t stream;
-};
-template <typename T, bool VEC, int NV>
-struct NormKernel {
-    static void launch(const NormLaunch& l) {
-        evo::fp8::add_rms_norm_kernel<T, VEC, NV><<<l.grid, 32 * l.s.warps, 0, l.stream>>>(l.p, l.s.wpr);
-    }
-};
+template <typename T, bool VEC, int NV, int R, int THREADS>
+void launch_norm_as(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {
+    auto kern = evo::fp8::add_rms_norm_kernel<T, VEC, NV, R, THREADS>;
+    const int grid = walking_grid(kern, s.threads, p.rows, s.threads / 32 / s.wpr * R);
+    kern<<<grid, s.threads, 0, stream>>>(p, s.wpr);
+}
+template <typename T, bool VEC>
+void launch_norm(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {
+    constexpr int R = sizeof(T) == 2 ? 2 : 1;    // fp32 rows fill the registers one at a time
+    if (s.threads > 256) return launch_norm_as<T, VEC, 4, 1, 1024>(p, s, stream);
+    if (s.wpr == 1) return launch_norm_as<T, VEC, 1, R, 256>(p, s, stream);
+    if (s.nv == 1) return launch_norm_as<T, VEC, 1, 1, 256>(p, s, stream);
+    if (s.nv == 2) return launch_norm_as<T, VEC, 2, 1, 256>(p, s, stream);
+    return launch_norm_as<T, VEC, 4, 1, 256>(p, s, stream);
+}
 
-struct NormBwdLaunch {
-    evo::fp8::NormBwdParams p;
-    RowSplit s;
-    int grid;
-    cudaStream_t stream;
-};
-template <typename T, bool VEC, int NV>
-struct NormBwdKernel {
-    static void launch(const NormBwdLaunch& l) {
-        const size_t shm = l.s.warps > l.s.wpr ? (size_t)l.s.warps * NV * 256 * sizeof(float) : 0;
-        evo::fp8::rms_bwd_kernel<T, VEC, NV><<<l.grid, 32 * l.s.warps, shm, l.stream>>>(l.p, l.s.wpr);
-    }
-};
+template <typename T, bool VEC, int NV, int R, int THREADS>
+void launch_norm_bwd_as(const evo::fp8::NormBwdParams& p, const RowSplit& s, int grid, cudaStream_t stream) {
+    const int warps = s.threads / 32;
+    const size_t shm = p.part && warps > s.wpr ? (size_t)warps * NV * 256 * sizeof(float) : 0;
+    evo::fp8::rms_bwd_kernel<T, VEC, NV, R, THREADS><<<grid, s.threads, shm, stream>>>(p, s.wpr);
+}
+template <typename T, bool VEC>
+void launch_norm_bwd(const evo::fp8::NormBwdParams& p, const RowSplit& s, int grid, cudaStream_t stream) {
+    constexpr int R = sizeof(T) == 2 ? 2 : 1;
+    if (s.threads > 640 || s.nv == 4) return launch_norm_bwd_as<T, VEC, 4, 1, 1024>(p, s, grid, stream);
+    if (s.nv == 2) return launch_norm_bwd_as<T, VEC, 2, 1, 640>(p, s, grid, stream);
+    if (s.wpr == 1) return launch_norm_bwd_as<T, VEC, 1, R, 256>(p, s, grid, stream);
+    return launch_norm_bwd_as<T, VEC, 1, 1, 640>(p, s, grid, stream);
+}
 // Blocks of the norm's backward, each of which leaves one partial row of d_weight: a pure
-// function of the sizes, because the workspace query answers from it.
+// function of the sizes (for the workspace query), for either type.
 int64_t norm_bwd_blocks(int64_t rows, int64_t cols) {
-    const RowSplit s = row_split(cols);
-    const int64_t per = s.warps / s.wpr;
-    return std::min<int64_t>((rows + per - 1) / per, 148 * (32 / s.warps));
+    const RowSplit s = row_split_bwd(cols);
+    const int64_t per = s.threads / 32 / s.wpr;
+    return std::min<int64_t>((rows + per - 1) / per, 148 * (s.threads <= 256 ? 2 : 1));
 }
 
 template <typename T, bool VEC>
@@ -472,10 +483,7 @@ evo_status_t quantize(const evo::fp8::QuantParams& p, evo_dtype_t dtype, bool sq
         return EVO_ERR_UNSUPPORTED;
     if ((p.rows + 127) / 128 > 0x7fffffff / ((p.cols + 127) / 128)) return EVO_ERR_UNSUPPORTED;
     const bool vec = rows_vec(p.x, p.rows, p.cols, p.ldx, e);
-    if (dtype == EVO_DTYPE_BF16)
-        vec ? launch_quantize<__nv_bfloat16, true>(p, square, s) : launch_quantize<__nv_bfloat16, false>(p, square, s);
-    else
-        vec ? launch_quantize<float, true>(p, square, s) : launch_quantize<float, false>(p, square, s);
+    by_type(dtype, vec, [&](auto t, auto v) { launch_quantize<decltype(t), decltype(v)::value>(p, square, s); });
     g_launches += 1;
     return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
@@ -931,19 +939,17 @@ evo_status_t evo_add_rms_norm_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype,
     for (const void* t : {x, residual, (const void*)h, (const void*)n})
         if (!aligned(t, e)) return EVO_ERR_INVALID_ARG;
     if (!aligned(weight, elem_bytes(w_dtype)) || !aligned(scale, 4) || !aligned(rstd, 4)) return EVO_ERR_INVALID_ARG;
-    NormLaunch l{};
-    l.p.rows = rows; l.p.cols = cols; l.p.x = x; l.p.res = residual; l.p.ldx = ldx; l.p.ldres = ldr;
-    l.p.w = weight; l.p.w_bf16 = w_dtype == EVO_DTYPE_BF16; l.p.eps = eps;
-    l.p.q = static_cast<uint8_t*>(q); l.p.ldq = ldq;
-    l.p.scale = scale; l.p.s_row = scale_row; l.p.s_grp = scale_group;
-    l.p.h = h; l.p.n = n; l.p.ldh = ldh; l.p.ldn = ldn; l.p.rstd = rstd;
-    l.s = row_split(cols);
-    const int64_t per = l.s.warps / l.s.wpr;
-    l.grid = (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * (64 / l.s.warps));
-    l.stream = static_cast<cudaStream_t>(stream);
+    evo::fp8::NormParams p{};
+    p.rows = rows; p.cols = cols; p.x = x; p.res = residual; p.ldx = ldx; p.ldres = ldr;
+    p.w = weight; p.w_bf16 = w_dtype == EVO_DTYPE_BF16; p.eps = eps; p.inv_cols = 1.0f / (float)cols;
+    p.q = static_cast<uint8_t*>(q); p.ldq = ldq;
+    p.scale = scale; p.s_row = scale_row; p.s_grp = scale_group;
+    p.h = h; p.n = n; p.ldh = ldh; p.ldn = ldn; p.rstd = rstd;
+    const RowSplit split = row_split(cols);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = rows_vec(x, rows, cols, ldx, e) && rows_vec(residual, rows, cols, ldr, e) &&
                      rows_vec(h, rows, cols, ldh, e) && rows_vec(n, rows, cols, ldn, e);
-    by_layout<NormKernel>(dtype, vec, l.s.nv, l);
+    by_type(dtype, vec, [&](auto t, auto v) { launch_norm<decltype(t), decltype(v)::value>(p, split, s); });
     g_launches += 1;
     return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
@@ -976,24 +982,23 @@ evo_status_t evo_add_rms_norm_bwd(int64_t rows, int64_t cols, evo_dtype_t dtype,
             return EVO_ERR_WORKSPACE_TOO_SMALL;
         if (!aligned(workspace, 16)) return EVO_ERR_INVALID_ARG;
     }
-    NormBwdLaunch l{};
-    l.p.rows = rows; l.p.cols = cols; l.p.dy = dy; l.p.dh = dh; l.p.h = h;
-    l.p.lddy = lddy; l.p.lddh = lddh; l.p.ldh = ldh; l.p.rstd = rstd;
-    l.p.w = weight; l.p.w_bf16 = w_dtype == EVO_DTYPE_BF16; l.p.dx = dx; l.p.lddx = lddx;
-    l.p.part = dweight ? static_cast<float*>(workspace) : nullptr;
-    l.s = row_split(cols);
-    l.grid = (int)norm_bwd_blocks(rows, cols);
-    l.stream = s;
+    evo::fp8::NormBwdParams p{};
+    p.rows = rows; p.cols = cols; p.dy = dy; p.dh = dh; p.h = h;
+    p.lddy = lddy; p.lddh = lddh; p.ldh = ldh; p.rstd = rstd;
+    p.w = weight; p.w_bf16 = w_dtype == EVO_DTYPE_BF16; p.inv_cols = 1.0f / (float)cols; p.dx = dx; p.lddx = lddx;
+    p.part = dweight ? static_cast<float*>(workspace) : nullptr;
+    const RowSplit split = row_split_bwd(cols);
+    const int blocks = (int)norm_bwd_blocks(rows, cols);
     const bool vec = rows_vec(dy, rows, cols, lddy, e) && rows_vec(dh, rows, cols, lddh, e) &&
                      rows_vec(h, rows, cols, ldh, e) && rows_vec(dx, rows, cols, lddx, e);
-    by_layout<NormBwdKernel>(dtype, vec, l.s.nv, l);
+    by_type(dtype, vec, [&](auto t, auto v) { launch_norm_bwd<decltype(t), decltype(v)::value>(p, split, blocks, s); });
     g_launches += 1;
     if (dweight) {
         const unsigned grid = (unsigned)((cols + 31) / 32);
         if (dw_dtype == EVO_DTYPE_BF16)
-            evo::fp8::sum_columns_kernel<<<grid, 1024, 0, s>>>(l.p.part, l.grid, cols, static_cast<__nv_bfloat16*>(dweight));
+            evo::fp8::sum_columns_kernel<<<grid, 1024, 0, s>>>(p.part, blocks, cols, static_cast<__nv_bfloat16*>(dweight));
         else
-            evo::fp8::sum_columns_kernel<<<grid, 1024, 0, s>>>(l.p.part, l.grid, cols, static_cast<float*>(dweight));
+            evo::fp8::sum_columns_kernel<<<grid, 1024, 0, s>>>(p.part, blocks, cols, static_cast<float*>(dweight));
         g_launches += 1;
     }
     return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;

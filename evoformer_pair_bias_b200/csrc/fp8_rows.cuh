@@ -7,16 +7,20 @@
 //
 // A group whose largest magnitude is m (held at LEAST or above) keeps
 //   q = e4m3(448 * v / m),   scale = m / 448.
-// The quotient is correctly rounded before the one rounding to e4m3: with
-// inv = 1/m rounded, q0 = t * inv and the remainder t - q0 * m taken by a fused
-// multiply-add, q0 + remainder * inv is the rounded quotient (Markstein's
-// correction step).  bf16 values make ties in e4m3 often enough to matter (448 =
+// The quotient is rounded once to fp32 before the one rounding to e4m3.  With
+// M = m / 512, t = 0.875 v and inv an approximate 1 / M, q0 = t * inv and the
+// remainder t - q0 * M by a fused multiply-add, q0 + remainder * inv is the
+// rounded quotient (Markstein's correction step; it leaves 2^-22 of a unit in the
+// last place).  bf16 values make ties in e4m3 often enough to matter (448 =
 // 7 * 64, so v = 3m/2^k is one); a plain product with 1/m would break them
-// either way.  t = 0.875 v cannot overflow and is exact for bf16 v; the factor
-// 512 that is left is exact.  In the norm the row's 1 / rms cancels out of
-// v / m, so the quotient is that of u = h * weight, exact in fp32 for bf16.
+// either way.  t is exact for bf16 v and cannot overflow, and neither M nor inv
+// leaves the normal range.  In the norm the row's 1 / rms cancels out of v / m,
+// so the quotient is that of u = h * weight, exact in fp32 for bf16.
 //
-// All of these move each byte once and are bound by HBM.
+// All of these move each byte once and are bound by HBM, next to it by the
+// instructions: at 6.4 TB/s an SM has some 17 issue slots a value, so sums and
+// products run on pairs (f32x2), bf16 adds on pairs too, and 1 / rms and 1 / M
+// come from the approximate unit (2^-22), which the quotient above corrects.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,33 +32,56 @@
 namespace evo {
 namespace fp8 {
 
+using sm100::f2;
+using sm100::f2hi;
+using sm100::f2lo;
+using sm100::fadd2;
+using sm100::ffma2;
+using sm100::fmul2;
+
 constexpr int GROUP = 128;
 constexpr float LEAST = 7.888609052210118e-31f;   // 2^-100: the smallest maximum a group is given
 constexpr float TOP = 448.0f;                     // largest e4m3 value
 
-// Two values as e4m3, `lo` in the low byte; NaN stays NaN.
+__device__ __forceinline__ uint64_t twice(float v) { return f2(v, v); }
+// Approximate reciprocal and reciprocal square root (hardware, normal range).
+__device__ __forceinline__ float fast_rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Two values as e4m3, the low one in the low byte; NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// 448 * v / m, correctly rounded; inv = 1 / m.
-__device__ __forceinline__ float quotient(float v, float m, float inv) {
-    const float t = 0.875f * v;
-    const float q = t * inv;
-    return fmaf(fmaf(-q, m, t), inv, q) * 512.0f;
+__device__ __forceinline__ uint32_t e4m3x2(uint64_t v) { return e4m3x2(f2lo(v), f2hi(v)); }
+// A group's divisor, ready for use on pairs: M = m / 512 (negated) and about 1 / M.
+__device__ __forceinline__ float neg_of(float m) { return m * (-1.0f / 512.0f); }
+__device__ __forceinline__ float inv_of(float m) { return fast_rcp(m * (1.0f / 512.0f)); }
+struct Divisor {
+    uint64_t neg, inv;
+    __device__ __forceinline__ explicit Divisor(float m) : neg(twice(neg_of(m))), inv(twice(inv_of(m))) {}
+    __device__ __forceinline__ Divisor(uint64_t n, uint64_t i) : neg(n), inv(i) {}   // another group for each of the pair
+};
+// 448 * v / m of a pair, rounded.
+__device__ __forceinline__ uint64_t quotient(uint64_t v, const Divisor& d) {
+    const uint64_t t = fmul2(v, twice(0.875f)), q = fmul2(t, d.inv);
+    return ffma2(ffma2(q, d.neg, t), d.inv, q);
 }
 // Four quotients as e4m3 bytes.
-__device__ __forceinline__ uint32_t e4m3x4(const float* v, float m, float inv) {
-    return e4m3x2(quotient(v[0], m, inv), quotient(v[1], m, inv)) |
-           (e4m3x2(quotient(v[2], m, inv), quotient(v[3], m, inv)) << 16);
+__device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b, const Divisor& d) {
+    return e4m3x2(quotient(a, d)) | (e4m3x2(quotient(b, d)) << 16);
 }
 // |v| as an integer that orders like it, with NaN above infinity above the rest:
 // the largest of a group is NaN as soon as one value is.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-// A group's maximum as a divisor: at least LEAST, NaN where it is not finite.
-__device__ __forceinline__ float divisor(uint32_t mag) {
-    return mag >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__uint_as_float(mag), LEAST);
+__device__ __forceinline__ uint32_t magnitude(uint64_t v) { return max(magnitude(f2lo(v)), magnitude(f2hi(v))); }
+// A group's maximum as a divisor: at least `least`, NaN where it is not finite.
+__device__ __forceinline__ float divisor(uint32_t mag, float least = LEAST) {
+    return mag >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__uint_as_float(mag), least);
 }
 
 // ------------------------------------------------------------- row fragments
@@ -63,83 +90,87 @@ __device__ __forceinline__ float divisor(uint32_t mag) {
 //   else  lane l holds columns l + 32e (single loads, coalesced): values 0..3 lie in
 //         the first group, 4..7 in the second
 // VEC wants every row 16-byte aligned and the row's bytes a multiple of 16.
+// Raw is a fragment as loaded, so that the next one can be on its way meanwhile.
 template <bool VEC>
 __device__ __forceinline__ int frag_col(int lane, int e) {
     return VEC ? 8 * lane + e : lane + 32 * e;
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_frag(const T* row, int64_t c0, int64_t cols, int lane, float* v) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        const int64_t c = c0 + 8 * lane;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (c < cols) w = *reinterpret_cast<const uint4*>(row + c);
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+    static constexpr bool PACKED = VEC && sizeof(T) == 2;
+    static constexpr int N = PACKED ? 4 : 8;     // words: bf16 pairs or floats
+    uint32_t w[N];
+
+    __device__ __forceinline__ void load(const T* row, int64_t c0, int64_t cols, int lane) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = sm100::bf16lo(a[e]);
-            v[2 * e + 1] = sm100::bf16hi(a[e]);
-        }
-    } else if constexpr (VEC) {
+            for (int h = 0; h < N / 4; ++h) {
+                const int64_t c = c0 + 8 * lane + 4 * h;
+                uint4 a = make_uint4(0, 0, 0, 0);
+                if (c < cols) a = *reinterpret_cast<const uint4*>(row + c);
+                w[4 * h] = a.x;
+                w[4 * h + 1] = a.y;
+                w[4 * h + 2] = a.z;
+                w[4 * h + 3] = a.w;
+            }
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t c = c0 + 8 * lane + 4 * h;
-            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c < cols) w = *reinterpret_cast<const float4*>(row + c);
-            v[4 * h] = w.x;
-            v[4 * h + 1] = w.y;
-            v[4 * h + 2] = w.z;
-            v[4 * h + 3] = w.w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t c = c0 + lane + 32 * e;
-            v[e] = c < cols ? Elem<T>::load(row + c) : 0.f;
+            for (int e = 0; e < 8; ++e) {
+                const int64_t c = c0 + lane + 32 * e;
+                w[e] = c < cols ? __float_as_uint(Elem<T>::load(row + c)) : 0u;
+            }
         }
     }
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_frag(T* row, int64_t c0, int64_t cols, int lane, const float* v) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        const int64_t c = c0 + 8 * lane;
-        if (c < cols)
-            *reinterpret_cast<uint4*>(row + c) =
-                make_uint4(sm100::pack_bf16(v[0], v[1]), sm100::pack_bf16(v[2], v[3]), sm100::pack_bf16(v[4], v[5]),
-                           sm100::pack_bf16(v[6], v[7]));
-    } else if constexpr (VEC) {
+    __device__ __forceinline__ void store(T* row, int64_t c0, int64_t cols, int lane) const {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t c = c0 + 8 * lane + 4 * h;
-            if (c < cols)
-                *reinterpret_cast<float4*>(row + c) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
-        }
-    } else {
+            for (int h = 0; h < N / 4; ++h) {
+                const int64_t c = c0 + 8 * lane + 4 * h;
+                if (c < cols) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t c = c0 + lane + 32 * e;
-            if (c < cols) Elem<T>::store(row + c, v[e]);
+            for (int e = 0; e < 8; ++e) {
+                const int64_t c = c0 + lane + 32 * e;
+                if (c < cols) Elem<T>::store(row + c, __uint_as_float(w[e]));
+            }
         }
     }
-}
-
-// v rounded to T and back.
-template <typename T>
-__device__ __forceinline__ float rounded(float v) {
-    if constexpr (sizeof(T) == 2) return __bfloat162float(__float2bfloat16_rn(v));
-    return v;
-}
+    // Values 2i and 2i + 1.
+    __device__ __forceinline__ uint64_t pair(int i) const {
+        if constexpr (PACKED) return sm100::bf16x2_to_f2(w[i]);
+        return f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    // Sets values 2i and 2i + 1, rounded to T.
+    __device__ __forceinline__ void set(int i, uint64_t v) {
+        if constexpr (PACKED) {
+            w[i] = sm100::pack_bf16(f2lo(v), f2hi(v));
+        } else if constexpr (sizeof(T) == 2) {
+            const uint32_t b = sm100::pack_bf16(f2lo(v), f2hi(v));
+            w[2 * i] = b << 16;
+            w[2 * i + 1] = b & 0xffff0000u;
+        } else {
+            w[2 * i] = __float_as_uint(f2lo(v));
+            w[2 * i + 1] = __float_as_uint(f2hi(v));
+        }
+    }
+    // this + o, rounded to T.
+    __device__ __forceinline__ void add(const Raw& o) {
+        if constexpr (PACKED) {                  // each half: one fp32 sum, rounded
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(o.w[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) set(i, fadd2(pair(i), o.pair(i)));
+        }
+    }
+};
 
 // Largest magnitude of each value's group: mag[0] for values 0..3, mag[1] for 4..7.
 template <bool VEC>
-__device__ __forceinline__ void group_max(const float* v, uint32_t* mag) {
-    uint32_t a = 0, b = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        a = max(a, magnitude(v[e]));
-        b = max(b, magnitude(v[4 + e]));
-    }
+__device__ __forceinline__ void group_max(const uint64_t* v, uint32_t* mag) {
+    uint32_t a = max(magnitude(v[0]), magnitude(v[1])), b = max(magnitude(v[2]), magnitude(v[3]));
     if (VEC) {                                   // one group in this half warp
         a = max(a, b);
 #pragma unroll
@@ -153,13 +184,18 @@ __device__ __forceinline__ void group_max(const float* v, uint32_t* mag) {
     mag[1] = b;
 }
 
-// The fragment's quotients, d[0] / d[1] the divisors of its two halves, as bytes of q's row.
+// The fragment's quotients, m[0] / m[1] the divisors of its two halves, as bytes of q's row.
 // q rows are 16-byte aligned; only columns below `cols` are written.
 template <bool VEC>
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int64_t c0, int64_t cols, int lane, const float* v,
-                                           const float* d) {
-    const float i0 = __frcp_rn(d[0]), i1 = VEC ? i0 : __frcp_rn(d[1]);
-    const uint32_t lo = e4m3x4(v, d[0], i0), hi = e4m3x4(v + 4, d[1], i1);
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int64_t c0, int64_t cols, int lane, const uint64_t* v,
+                                           const float* m) {
+    const Divisor d0(m[0]);
+    const uint32_t lo = e4m3x4(v[0], v[1], d0);
+    uint32_t hi;
+    if (VEC)
+        hi = e4m3x4(v[2], v[3], d0);
+    else
+        hi = e4m3x4(v[2], v[3], Divisor(m[1]));
     if (VEC) {
         const int64_t c = c0 + 8 * lane;
         if (c + 8 <= cols)
@@ -193,7 +229,7 @@ struct NormParams {
     int64_t ldx, ldres;
     const void* w;               // [cols], bf16 or fp32, or null (ones)
     int w_bf16;
-    float eps;
+    float eps, inv_cols;
     uint8_t* q;                  // e4m3 [rows, cols]
     int64_t ldq;
     float* scale;                // [rows, groups] with strides
@@ -207,85 +243,115 @@ __device__ __forceinline__ float load_w(const void* w, int bf16, int64_t c) {
     if (!w) return 1.f;
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]) : static_cast<const float*>(w)[c];
 }
+// The weight of a lane's columns, in pairs; zero beyond the row.
+template <bool VEC, int NV>
+__device__ __forceinline__ void load_weight(const void* w, int bf16, int64_t cols, int wpr, int part, int lane,
+                                            uint64_t (*out)[4]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t c0 = (int64_t)(i * wpr + part) * 256;
+            const int64_t a = c0 + frag_col<VEC>(lane, 2 * e), b = c0 + frag_col<VEC>(lane, 2 * e + 1);
+            out[i][e] = f2(a < cols ? load_w(w, bf16, a) : 0.f, b < cols ? load_w(w, bf16, b) : 0.f);
+        }
+}
 
-// Sum of one value per lane over the `wpr` warps of a row (a power of two).  Every warp of
-// the block calls it; `slot` alternates so that one barrier per call is enough.
-__device__ __forceinline__ float row_sum(float v, int wpr, int warp, float* buf) {
+// Sum of one value per lane over the `wpr` warps of a row, the first of them `first`.  Every warp
+// of the block calls it; the caller alternates `buf`, so that one barrier per call is enough.
+__device__ __forceinline__ float row_sum(float v, int wpr, int warp, int first, float* buf) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (wpr == 1) return v;
     if ((threadIdx.x & 31) == 0) buf[warp] = v;
     __syncthreads();
-    const int w0 = warp & ~(wpr - 1);
     float s = 0.f;
-    for (int i = 0; i < wpr; ++i) s += buf[w0 + i];
+    for (int i = 0; i < wpr; ++i) s += buf[first + i];
     return s;
 }
 
-// wpr warps (a power of two) hold a row, NV fragments of 256 columns each; a block holds
-// (blockDim / 32) / wpr rows at a time and walks the rows with the grid.  The weight stays
-// in registers.
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p, const int wpr) {
+// A row lies with wpr warps, NV fragments of 256 columns each; a block of at most THREADS threads
+// takes blockDim / 32 / wpr * R rows at a time (R rows per warp, only with wpr == 1) and walks the
+// rows with the grid.  The weight stays in registers, and the next rows are loaded while these are
+// worked on: at 32 warps of one row an SM has 32 KB on its way, too little for HBM's latency
+// (196608 x 256 in bf16: 104 us, with the loads ahead TODO).
+template <typename T, bool VEC, int NV, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 && NV * R <= 2 ? 2 : 1) add_rms_norm_kernel(const NormParams p, const int wpr) {
     __shared__ float buf[2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (blockDim.x >> 5) / wpr, sub = warp / wpr, part = warp & (wpr - 1);
-    float w[NV][8];
+    const int first = warp / wpr * wpr, part = warp - first;
+    const int per = (int)(blockDim.x >> 5) / wpr * R, sub = warp / wpr * R;
+    const int64_t step = (int64_t)gridDim.x * per;
+    uint64_t w[NV][4];
+    load_weight<VEC, NV>(p.w, p.w_bf16, p.cols, wpr, part, lane, w);
+    Raw<T, VEC> x[R][NV], res[R][NV];
+    auto load = [&](int64_t r) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+        for (int k = 0; k < R; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t c = (int64_t)(i * wpr + part) * 256 + frag_col<VEC>(lane, e);
-            w[i][e] = c < p.cols ? load_w(p.w, p.w_bf16, c) : 0.f;
-        }
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c0 = (int64_t)(i * wpr + part) * 256, lim = r + k < p.rows ? p.cols : 0;
+                x[k][i].load(static_cast<const T*>(p.x) + (r + k) * p.ldx, c0, lim, lane);
+                if (p.res) res[k][i].load(static_cast<const T*>(p.res) + (r + k) * p.ldres, c0, lim, lane);
+            }
+    };
+    int64_t r = (int64_t)blockIdx.x * per + sub;
+    load(r);
     int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per, turn ^= 1) {
-        const int64_t r = r0 + sub;
-        const bool live = r < p.rows;
-        float h[NV][8];
-        float sq = 0.f;
+    // every warp makes the same number of turns, for the barrier in row_sum
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += step, r += step, turn ^= 1) {
+        Raw<T, VEC> h[R][NV];
+        float rstd[R], least[R], per_m[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c0 = (int64_t)(i * wpr + part) * 256;
-            const int64_t lim = live ? p.cols : 0;
-            load_frag<T, VEC>(static_cast<const T*>(p.x) + r * p.ldx, c0, lim, lane, h[i]);
-            if (p.res) {
-                float a[8];
-                load_frag<T, VEC>(static_cast<const T*>(p.res) + r * p.ldres, c0, lim, lane, a);
+        for (int k = 0; k < R; ++k)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] = rounded<T>(h[i][e] + a[e]);
+            for (int i = 0; i < NV; ++i) {
+                h[k][i] = x[k][i];
+                if (p.res) h[k][i].add(res[k][i]);
             }
+        load(r + step);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sq = fmaf(h[i][e], h[i][e], sq);
+        for (int k = 0; k < R; ++k) {
+            uint64_t sq = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sq = ffma2(h[k][i].pair(e), h[k][i].pair(e), sq);
+            const float ms = row_sum(f2lo(sq) + f2hi(sq), wpr, warp, first, buf[turn]) * p.inv_cols + p.eps;
+            rstd[k] = rsqrtf(ms);
+            least[k] = LEAST * ms * rstd[k];               // LEAST / rstd: the least maximum of u = n / rstd
+            per_m[k] = least[k] == least[k] ? rstd[k] * (1.0f / TOP) : least[k];   // NaN where ms is 0 or infinite
         }
-        sq = row_sum(sq, wpr, warp, buf[turn]);
-        const float rstd = __frsqrt_rn(__fdiv_rn(sq, (float)p.cols) + p.eps);
-        if (!live) continue;                     // no barrier below
-        const float floor_u = __fdiv_rn(LEAST, rstd);
-        if (p.rstd && part == 0 && lane == 0) p.rstd[r] = rstd;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c0 = (int64_t)(i * wpr + part) * 256;
-            if (c0 >= p.cols) break;
-            if (p.h) store_frag<T, VEC>(static_cast<T*>(p.h) + r * p.ldh, c0, p.cols, lane, h[i]);
-            if (p.n) {
-                float n[8];
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = r + k;
+            if (row >= p.rows) continue;                   // no barrier below
+            if (p.rstd && part == 0 && lane == 0) p.rstd[row] = rstd[k];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) n[e] = h[i][e] * rstd * w[i][e];
-                store_frag<T, VEC>(static_cast<T*>(p.n) + r * p.ldn, c0, p.cols, lane, n);
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c0 = (int64_t)(i * wpr + part) * 256;
+                if (c0 >= p.cols) break;
+                if (p.h) h[k][i].store(static_cast<T*>(p.h) + row * p.ldh, c0, p.cols, lane);
+                uint64_t u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[e] = fmul2(h[k][i].pair(e), w[i][e]);
+                if (p.n) {
+                    Raw<T, VEC> n;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) n.set(e, fmul2(u[e], twice(rstd[k])));
+                    n.store(static_cast<T*>(p.n) + row * p.ldn, c0, p.cols, lane);
+                }
+                uint32_t mag[2];
+                group_max<VEC>(u, mag);
+                float m[2], sc[2];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    m[g] = divisor(mag[g], least[k]);
+                    sc[g] = m[g] * per_m[k];
+                }
+                store_e4m3<VEC>(p.q + row * p.ldq, c0, p.cols, lane, u, m);
+                store_scales<VEC>(p.scale + row * p.s_row, p.s_grp, c0, p.cols, lane, sc);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] *= w[i][e];
-            uint32_t mag[2];
-            group_max<VEC>(h[i], mag);
-            float d[2], sc[2];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                d[g] = mag[g] >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : fmaxf(__uint_as_float(mag[g]), floor_u);
-                sc[g] = __fdiv_rn(d[g] * rstd, TOP);
-            }
-            store_e4m3<VEC>(p.q + r * p.ldq, c0, p.cols, lane, h[i], d);
-            store_scales<VEC>(p.scale + r * p.s_row, p.s_grp, c0, p.cols, lane, sc);
         }
     }
 }
@@ -298,6 +364,7 @@ struct NormBwdParams {
     const float* rstd;           // [rows]
     const void* w;
     int w_bf16;
+    float inv_cols;
     void* dx;                    // T [rows, cols]
     int64_t lddx;
     float* part;                 // fp32 [gridDim.x, cols] partial sums of d_weight, or null
@@ -306,85 +373,112 @@ struct NormBwdParams {
 // dx = dh + rstd * (g - n * mean(g n)), g = dy * w, n = h * rstd.  Each warp adds up dy * n of
 // the rows it meets in registers; a block's rows are joined in shared memory and leave one
 // partial row, and sum_columns_kernel adds the partial rows in order: no atomics, the same
-// bits on every run.
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(1024) rms_bwd_kernel(const NormBwdParams p, const int wpr) {
+// bits on every run.  Layout and loads ahead as in the forward.
+template <typename T, bool VEC, int NV, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rms_bwd_kernel(const NormBwdParams p, const int wpr) {
     __shared__ float buf[2][32];
     extern __shared__ float join[];              // [warps][NV][256] when a block holds several rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (blockDim.x >> 5) / wpr, sub = warp / wpr, part = warp & (wpr - 1);
-    float w[NV][8], dw[NV][8];
+    const int first = warp / wpr * wpr, part = warp - first;
+    const int rows_b = (int)(blockDim.x >> 5) / wpr, per = rows_b * R, sub = warp / wpr * R;
+    const int64_t step = (int64_t)gridDim.x * per;
+    uint64_t w[NV][4], dw[NV][4];
+    load_weight<VEC, NV>(p.w, p.w_bf16, p.cols, wpr, part, lane, w);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t c = (int64_t)(i * wpr + part) * 256 + frag_col<VEC>(lane, e);
-            w[i][e] = c < p.cols ? load_w(p.w, p.w_bf16, c) : 0.f;
-            dw[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) dw[i][e] = 0;
+    Raw<T, VEC> dy[R][NV], h[R][NV], dh[R][NV];
+    float rs[R];
+    auto load = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const bool live = r + k < p.rows;
+            rs[k] = live ? p.rstd[r + k] : 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c0 = (int64_t)(i * wpr + part) * 256, lim = live ? p.cols : 0;
+                dy[k][i].load(static_cast<const T*>(p.dy) + (r + k) * p.lddy, c0, lim, lane);
+                h[k][i].load(static_cast<const T*>(p.h) + (r + k) * p.ldh, c0, lim, lane);
+                if (p.dh) dh[k][i].load(static_cast<const T*>(p.dh) + (r + k) * p.lddh, c0, lim, lane);
+            }
         }
+    };
+    int64_t r = (int64_t)blockIdx.x * per + sub;
+    load(r);
     int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per, turn ^= 1) {
-        const int64_t r = r0 + sub;
-        const bool live = r < p.rows;
-        const float rstd = live ? p.rstd[r] : 0.f;
-        float dy[NV][8], n[NV][8];
-        float dot = 0.f;
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += step, r += step, turn ^= 1) {
+        uint64_t g[R][NV][4], n[R][NV][4], a[R][NV][4];
+        float rstd[R], mean[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c0 = (int64_t)(i * wpr + part) * 256;
-            const int64_t lim = live ? p.cols : 0;
-            load_frag<T, VEC>(static_cast<const T*>(p.dy) + r * p.lddy, c0, lim, lane, dy[i]);
-            load_frag<T, VEC>(static_cast<const T*>(p.h) + r * p.ldh, c0, lim, lane, n[i]);
+        for (int k = 0; k < R; ++k) {
+            rstd[k] = rs[k];
+            const uint64_t rs2 = twice(rs[k]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                n[i][e] *= rstd;
-                if (live) dw[i][e] = fmaf(dy[i][e], n[i][e], dw[i][e]);
-                dy[i][e] *= w[i][e];
-                dot = fmaf(dy[i][e], n[i][e], dot);
-            }
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {              // a row past the end is all zeros
+                    n[k][i][e] = fmul2(h[k][i].pair(e), rs2);
+                    const uint64_t y = dy[k][i].pair(e);
+                    dw[i][e] = ffma2(y, n[k][i][e], dw[i][e]);
+                    g[k][i][e] = fmul2(y, w[i][e]);
+                    a[k][i][e] = p.dh ? dh[k][i].pair(e) : 0;
+                }
         }
-        dot = row_sum(dot, wpr, warp, buf[turn]);
-        if (!live) continue;
-        const float mean = __fdiv_rn(dot, (float)p.cols);
+        load(r + step);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c0 = (int64_t)(i * wpr + part) * 256;
-            if (c0 >= p.cols) break;
-            float a[8];
-            if (p.dh) {
-                load_frag<T, VEC>(static_cast<const T*>(p.dh) + r * p.lddh, c0, p.cols, lane, a);
-            } else {
+        for (int k = 0; k < R; ++k) {
+            uint64_t dot = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] = 0.f;
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dot = ffma2(g[k][i][e], n[k][i][e], dot);
+            mean[k] = row_sum(f2lo(dot) + f2hi(dot), wpr, warp, first, buf[turn]) * p.inv_cols;
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = r + k;
+            if (row >= p.rows) continue;
+            const uint64_t neg = twice(-mean[k]), rs2 = twice(rstd[k]);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c0 = (int64_t)(i * wpr + part) * 256;
+                if (c0 >= p.cols) break;
+                Raw<T, VEC> o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o.set(e, ffma2(rs2, ffma2(n[k][i][e], neg, g[k][i][e]), a[k][i][e]));
+                o.store(static_cast<T*>(p.dx) + row * p.lddx, c0, p.cols, lane);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] = fmaf(rstd, fmaf(-n[i][e], mean, dy[i][e]), a[e]);
-            store_frag<T, VEC>(static_cast<T*>(p.dx) + r * p.lddx, c0, p.cols, lane, a);
         }
     }
     if (!p.part) return;
     float* out = p.part + (int64_t)blockIdx.x * p.cols;
-    if (per > 1) {
+    if (rows_b > 1) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) join[(warp * NV + i) * 256 + frag_col<VEC>(lane, e)] = dw[i][e];
+            for (int e = 0; e < 4; ++e) {
+                join[(warp * NV + i) * 256 + frag_col<VEC>(lane, 2 * e)] = f2lo(dw[i][e]);
+                join[(warp * NV + i) * 256 + frag_col<VEC>(lane, 2 * e + 1)] = f2hi(dw[i][e]);
+            }
         __syncthreads();
         // column c of the row lies with warp (c / 256) % wpr of each row, fragment (c / 256) / wpr
         for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
-            const int f = (int)(c >> 8), o = ((f & (wpr - 1)) * NV + f / wpr) * 256 + (int)(c & 255);
+            const int f = (int)(c >> 8), o = (f % wpr * NV + f / wpr) * 256 + (int)(c & 255);
             float s = 0.f;
-            for (int k = 0; k < per; ++k) s += join[k * wpr * NV * 256 + o];
+            for (int k = 0; k < rows_b; ++k) s += join[k * wpr * NV * 256 + o];
             out[c] = s;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t c = (int64_t)(i * wpr + part) * 256 + frag_col<VEC>(lane, e);
-                if (c < p.cols) out[c] = dw[i][e];
+            for (int e = 0; e < 4; ++e) {
+                const int64_t c0 = (int64_t)(i * wpr + part) * 256;
+                const int64_t ca = c0 + frag_col<VEC>(lane, 2 * e), cb = c0 + frag_col<VEC>(lane, 2 * e + 1);
+                if (ca < p.cols) out[ca] = f2lo(dw[i][e]);
+                if (cb < p.cols) out[cb] = f2hi(dw[i][e]);
             }
     }
 }
@@ -428,19 +522,29 @@ struct QuantParams {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
     const int lane = threadIdx.x & 31;
-    const int64_t chunks = (p.cols + 255) / 256, items = p.rows * chunks;
-    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < items; t += (int64_t)gridDim.x * 8) {
+    const int64_t chunks = (p.cols + 255) / 256, items = p.rows * chunks, step = (int64_t)gridDim.x * 8;
+    int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    Raw<T, VEC> next;
+    auto load = [&](int64_t at) {
+        const int64_t r = at / chunks;
+        next.load(static_cast<const T*>(p.x) + r * p.ldx, (at - r * chunks) * 256, at < items ? p.cols : 0, lane);
+    };
+    load(t);
+    for (; t < items; t += step) {
         const int64_t r = t / chunks, c0 = (t - r * chunks) * 256;
-        float v[8], d[2], sc[2];
-        load_frag<T, VEC>(static_cast<const T*>(p.x) + r * p.ldx, c0, p.cols, lane, v);
+        uint64_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = next.pair(e);
+        load(t + step);
         uint32_t mag[2];
         group_max<VEC>(v, mag);
+        float m[2], sc[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            d[g] = divisor(mag[g]);
-            sc[g] = __fdiv_rn(d[g], TOP);
+            m[g] = divisor(mag[g]);
+            sc[g] = m[g] * (1.0f / TOP);
         }
-        store_e4m3<VEC>(p.q + r * p.ldq, c0, p.cols, lane, v, d);
+        store_e4m3<VEC>(p.q + r * p.ldq, c0, p.cols, lane, v, m);
         store_scales<VEC>(p.scale + r * p.s_row, p.s_grp, c0, p.cols, lane, sc);
     }
 }
@@ -483,9 +587,15 @@ struct Tile {
             }
         }
     }
-    __device__ __forceinline__ float at(int i, int j) const {
-        if constexpr (PACKED) return j & 1 ? sm100::bf16hi(v[i][j / 2]) : sm100::bf16lo(v[i][j / 2]);
-        return __uint_as_float(v[i][j]);
+    // Columns 2j and 2j + 1 of row i.
+    __device__ __forceinline__ uint64_t pair(int i, int j) const {
+        if constexpr (PACKED) return sm100::bf16x2_to_f2(v[i][j]);
+        return f2(__uint_as_float(v[i][2 * j]), __uint_as_float(v[i][2 * j + 1]));
+    }
+    // Where word w (four rows) of column c lies in the transposed tile: rotated by the column, so
+    // that a warp's words, and a column's, meet 32 banks.
+    static __device__ __forceinline__ int spot(int c, int w) {
+        return c * 32 + (w ^ (PACKED ? c >> 3 << 1 : VEC ? c >> 2 : c & 31));
     }
     // Magnitudes as integers that order like them: pairs of 16 bits (PACKED) or one of 32.
     static __device__ __forceinline__ uint32_t mag(uint32_t w) { return w & (PACKED ? 0x7fff7fffu : 0x7fffffffu); }
@@ -499,14 +609,13 @@ struct Tile {
 // 128 x 128 blocks (SQUARE), or 1 x 128 groups along the columns for q and along the rows for the
 // transpose.  ROWS writes q, TRANSPOSE the transpose, through shared memory.
 template <typename T, bool VEC, bool SQUARE, bool ROWS, bool TRANSPOSE>
-__global__ void __launch_bounds__(512, 2) quantize_tile_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !ROWS ? 3 : 2) quantize_tile_kernel(const QuantParams p) {
     using L = Tile<T, VEC>;
-    constexpr int PITCH = 132;                   // bytes of a transposed column: 33 words, so columns meet other banks
     constexpr int W = L::PACKED ? 64 : 128;      // words of a warp's column maxima
     constexpr bool BY_COL = TRANSPOSE && !SQUARE;
     __shared__ uint32_t cmax[BY_COL ? 16 : 1][BY_COL ? W + 2 : 16];
-    __shared__ float dv[BY_COL ? 128 : 1], iv[BY_COL ? 128 : 1];
-    __shared__ uint32_t tq[TRANSPOSE ? 128 * PITCH / 4 : 1];
+    __shared__ __align__(16) float dv[BY_COL ? 256 : 1];   // BY_COL: M and 1 / M of columns 2c, 2c + 1 side by side
+    __shared__ uint32_t tq[TRANSPOSE ? 128 * 32 : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t tc = (p.cols + 127) / 128;
     const int64_t br = blockIdx.x / tc, bc = blockIdx.x - br * tc;
@@ -527,9 +636,8 @@ __global__ void __launch_bounds__(512, 2) quantize_tile_kernel(const QuantParams
             if (lane == 0) {
                 const float d = divisor(m);
                 dv[0] = d;
-                iv[0] = __frcp_rn(d);
-                if (ROWS) p.scale[br * p.s_row + bc * p.s_grp] = __fdiv_rn(d, TOP);
-                if (TRANSPOSE) p.scale_t[bc * p.st_row + br * p.st_grp] = __fdiv_rn(d, TOP);
+                if (ROWS) p.scale[br * p.s_row + bc * p.s_grp] = d * (1.0f / TOP);
+                if (TRANSPOSE) p.scale_t[bc * p.st_row + br * p.st_grp] = d * (1.0f / TOP);
             }
         }
         __syncthreads();
@@ -557,22 +665,34 @@ __global__ void __launch_bounds__(512, 2) quantize_tile_kernel(const QuantParams
         if (L::PACKED) a = c & 1 ? a & 0xffff0000u : a << 16;
         if (part == 0) {
             const float d = divisor(a);
-            dv[c] = d;
-            iv[c] = __frcp_rn(d);
-            if (c0 + c < p.cols) p.scale_t[(c0 + c) * p.st_row + br * p.st_grp] = __fdiv_rn(d, TOP);
+            dv[(c >> 1) * 4 + (c & 1)] = neg_of(d);
+            dv[(c >> 1) * 4 + 2 + (c & 1)] = inv_of(d);
+            if (c0 + c < p.cols) p.scale_t[(c0 + c) * p.st_row + br * p.st_grp] = d * (1.0f / TOP);
         }
         __syncthreads();
     }
     const int rr = L::row(warp, lane);
     if constexpr (TRANSPOSE) {
 #pragma unroll
-        for (int j = 0; j < L::TC; ++j) {
-            const int c = L::col(lane, j);
-            const float d = dv[SQUARE ? 0 : c], inv = iv[SQUARE ? 0 : c];
+        for (int j = 0; j < L::TC / 2; ++j) {
+            const int c = L::col(lane, 2 * j), c1 = L::col(lane, 2 * j + 1);
+            Divisor d(0, 0);
+            if constexpr (SQUARE) {
+                d = Divisor(dv[0]);
+            } else if constexpr (VEC) {
+                const float4 f = *reinterpret_cast<const float4*>(dv + 2 * c);
+                d = Divisor(f2(f.x, f.y), f2(f.z, f.w));
+            } else {
+                const int a = (c >> 1) * 4 + (c & 1), b = (c1 >> 1) * 4 + (c1 & 1);
+                d = Divisor(f2(dv[a], dv[b]), f2(dv[a + 2], dv[b + 2]));
+            }
 #pragma unroll
             for (int i = 0; i < L::TR; i += 4) {
-                const float f[4] = {t.at(i, j), t.at(i + 1, j), t.at(i + 2, j), t.at(i + 3, j)};
-                tq[c * (PITCH / 4) + (rr + i) / 4] = e4m3x4(f, d, inv);
+                uint64_t q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) q[k] = quotient(t.pair(i + k, j), d);
+                tq[L::spot(c, (rr + i) / 4)] = e4m3x2(f2lo(q[0]), f2lo(q[1])) | (e4m3x2(f2lo(q[2]), f2lo(q[3])) << 16);
+                tq[L::spot(c1, (rr + i) / 4)] = e4m3x2(f2hi(q[0]), f2hi(q[1])) | (e4m3x2(f2hi(q[2]), f2hi(q[3])) << 16);
             }
         }
         __syncthreads();
@@ -583,7 +703,7 @@ __global__ void __launch_bounds__(512, 2) quantize_tile_kernel(const QuantParams
             const int c = warp * 8 + k;
             if (c0 + c >= p.cols) break;
             uint8_t* out = p.qt + (c0 + c) * p.ldqt + r;
-            const uint32_t b = tq[c * (PITCH / 4) + lane];
+            const uint32_t b = tq[L::spot(c, lane)];
             if (r + 4 <= p.rows) {
                 *reinterpret_cast<uint32_t*>(out) = b;
             } else {
@@ -596,7 +716,7 @@ __global__ void __launch_bounds__(512, 2) quantize_tile_kernel(const QuantParams
 #pragma unroll
         for (int i = 0; i < L::TR; ++i) {
             const int64_t r = r0 + rr + i;
-            float d = SQUARE ? dv[0] : 0.f, inv = SQUARE ? iv[0] : 0.f;
+            float m_row = SQUARE ? dv[0] : 0.f;
             if constexpr (!SQUARE) {             // the row's group: 16 or 32 lanes hold it
                 uint32_t m = 0;
 #pragma unroll
@@ -608,25 +728,25 @@ __global__ void __launch_bounds__(512, 2) quantize_tile_kernel(const QuantParams
 #pragma unroll
                     for (int o = 8; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                 }
-                d = divisor(m);
-                inv = __frcp_rn(d);
-                if (lane % L::LPR == 0 && r < p.rows) p.scale[r * p.s_row + bc * p.s_grp] = __fdiv_rn(d, TOP);
+                m_row = divisor(m);
+                if (lane % L::LPR == 0 && r < p.rows) p.scale[r * p.s_row + bc * p.s_grp] = m_row * (1.0f / TOP);
             }
             if (r >= p.rows) continue;
             uint8_t* out = p.q + r * p.ldq;
-            float f[L::TC];
+            const Divisor d(m_row);
+            uint64_t f[L::TC / 2];
 #pragma unroll
-            for (int j = 0; j < L::TC; ++j) f[j] = t.at(i, j);
+            for (int j = 0; j < L::TC / 2; ++j) f[j] = t.pair(i, j);
             if constexpr (VEC) {
                 const int64_t c = c0 + L::col(lane, 0);
                 if (c < p.cols) {
                     if constexpr (L::TC == 8)
-                        *reinterpret_cast<uint2*>(out + c) = make_uint2(e4m3x4(f, d, inv), e4m3x4(f + 4, d, inv));
+                        *reinterpret_cast<uint2*>(out + c) = make_uint2(e4m3x4(f[0], f[1], d), e4m3x4(f[2], f[3], d));
                     else
-                        *reinterpret_cast<uint32_t*>(out + c) = e4m3x4(f, d, inv);
+                        *reinterpret_cast<uint32_t*>(out + c) = e4m3x4(f[0], f[1], d);
                 }
             } else {
-                const uint32_t b = e4m3x4(f, d, inv);
+                const uint32_t b = e4m3x4(f[0], f[1], d);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int64_t c = c0 + L::col(lane, j);
