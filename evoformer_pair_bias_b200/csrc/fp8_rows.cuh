@@ -565,25 +565,23 @@ struct Tile {
     static __device__ __forceinline__ int row(int warp, int lane) { return warp * 8 + (lane / LPR) * TR; }
 
     __device__ __forceinline__ void load(const QuantParams& p, int64_t r0, int64_t c0, int warp, int lane) {
-        const int64_t r = r0 + row(warp, lane);
+        const int64_t r = r0 + row(warp, lane), c = c0 + col(lane, 0);
+        const int rows = (int)min((int64_t)TR, p.rows - r);
+        const T* x = static_cast<const T*>(p.x) + r * p.ldx + (VEC ? c : c0);
 #pragma unroll
-        for (int i = 0; i < TR; ++i) {
-            const T* x = static_cast<const T*>(p.x) + (r + i) * p.ldx;
-            const bool live = r + i < p.rows;
+        for (int i = 0; i < TR; ++i, x += p.ldx) {
+            const bool live = i < rows && c < p.cols;
             if constexpr (VEC) {
-                const int64_t c = c0 + col(lane, 0);
                 uint4 w = make_uint4(0, 0, 0, 0);
-                if (live && c < p.cols) w = *reinterpret_cast<const uint4*>(x + c);
+                if (live) w = *reinterpret_cast<const uint4*>(x);
                 v[i][0] = w.x;
                 v[i][1] = w.y;
                 v[i][2] = w.z;
                 v[i][3] = w.w;
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t c = c0 + col(lane, j);
-                    v[i][j] = live && c < p.cols ? __float_as_uint(Elem<T>::load(x + c)) : 0u;
-                }
+                for (int j = 0; j < 4; ++j)
+                    v[i][j] = live && c + 32 * j < p.cols ? __float_as_uint(Elem<T>::load(x + col(lane, j))) : 0u;
             }
         }
     }
@@ -592,14 +590,23 @@ struct Tile {
         if constexpr (PACKED) return sm100::bf16x2_to_f2(v[i][j]);
         return f2(__uint_as_float(v[i][2 * j]), __uint_as_float(v[i][2 * j + 1]));
     }
-    // Where word w (four rows) of column c lies in the transposed tile: rotated by the column, so
-    // that a warp's words, and a column's, meet 32 banks.
-    static __device__ __forceinline__ int spot(int c, int w) {
-        return c * 32 + (w ^ (PACKED ? c >> 3 << 1 : VEC ? c >> 2 : c & 31));
+    // Where word w (four rows) of column c lies in the transposed tile: rotated by the lane that
+    // writes the column, so that a warp's words, and a column's, meet 32 banks.
+    static __device__ __forceinline__ int owner(int c) { return PACKED ? c >> 3 : VEC ? c >> 2 : c & 31; }
+    static __device__ __forceinline__ int spot(int c, int w) { return c * 32 + (w ^ (PACKED ? 2 * owner(c) : owner(c))); }
+    // The divisors of a lane's j-th column pair lie together, those of the lanes side by side: index
+    // of column c's float (its M, and two further its 1 / M).
+    static __device__ __forceinline__ int pair_at(int lane, int j) { return 4 * (j * LPR + lane % LPR); }
+    static __device__ __forceinline__ int divisor_at(int c) {
+        return VEC ? pair_at(owner(c), (c % TC) >> 1) + (c & 1) : pair_at(c & 31, c >> 6) + ((c >> 5) & 1);
     }
     // Magnitudes as integers that order like them: pairs of 16 bits (PACKED) or one of 32.
     static __device__ __forceinline__ uint32_t mag(uint32_t w) { return w & (PACKED ? 0x7fff7fffu : 0x7fffffffu); }
-    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return PACKED ? __vmaxu2(a, b) : max(a, b); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        if (!PACKED) return max(a, b);
+        asm("max.u16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        return a;
+    }
     // The larger of a pair (PACKED), as the bits of a float.
     static __device__ __forceinline__ uint32_t widest(uint32_t m) {
         return PACKED ? max(m << 16, m & 0xffff0000u) : m;
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !ROWS ? 3 : 2) qu
     constexpr int W = L::PACKED ? 64 : 128;      // words of a warp's column maxima
     constexpr bool BY_COL = TRANSPOSE && !SQUARE;
     __shared__ uint32_t cmax[BY_COL ? 16 : 1][BY_COL ? W + 2 : 16];
-    __shared__ __align__(16) float dv[BY_COL ? 256 : 1];   // BY_COL: M and 1 / M of columns 2c, 2c + 1 side by side
+    __shared__ __align__(16) float dv[BY_COL ? 256 : 1];   // BY_COL: M and 1 / M of every column
     __shared__ uint32_t tq[TRANSPOSE ? 128 * 32 : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t tc = (p.cols + 127) / 128;
@@ -665,8 +672,8 @@ __global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !ROWS ? 3 : 2) qu
         if (L::PACKED) a = c & 1 ? a & 0xffff0000u : a << 16;
         if (part == 0) {
             const float d = divisor(a);
-            dv[(c >> 1) * 4 + (c & 1)] = neg_of(d);
-            dv[(c >> 1) * 4 + 2 + (c & 1)] = inv_of(d);
+            dv[L::divisor_at(c)] = neg_of(d);
+            dv[L::divisor_at(c) + 2] = inv_of(d);
             if (c0 + c < p.cols) p.scale_t[(c0 + c) * p.st_row + br * p.st_grp] = d * (1.0f / TOP);
         }
         __syncthreads();
@@ -679,12 +686,9 @@ __global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !ROWS ? 3 : 2) qu
             Divisor d(0, 0);
             if constexpr (SQUARE) {
                 d = Divisor(dv[0]);
-            } else if constexpr (VEC) {
-                const float4 f = *reinterpret_cast<const float4*>(dv + 2 * c);
-                d = Divisor(f2(f.x, f.y), f2(f.z, f.w));
             } else {
-                const int a = (c >> 1) * 4 + (c & 1), b = (c1 >> 1) * 4 + (c1 & 1);
-                d = Divisor(f2(dv[a], dv[b]), f2(dv[a + 2], dv[b + 2]));
+                const float4 f = *reinterpret_cast<const float4*>(dv + L::pair_at(lane, j));
+                d = Divisor(f2(f.x, f.y), f2(f.z, f.w));
             }
 #pragma unroll
             for (int i = 0; i < L::TR; i += 4) {
@@ -698,13 +702,14 @@ __global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !ROWS ? 3 : 2) qu
         __syncthreads();
         // a warp writes 128 bytes of an output row at a time
         const int64_t r = r0 + 4 * lane;
+        const int cols = (int)min((int64_t)8, p.cols - c0 - warp * 8);
+        uint8_t* out = p.qt + (c0 + warp * 8) * p.ldqt + r;
+        const bool whole = r + 4 <= p.rows;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int c = warp * 8 + k;
-            if (c0 + c >= p.cols) break;
-            uint8_t* out = p.qt + (c0 + c) * p.ldqt + r;
-            const uint32_t b = tq[L::spot(c, lane)];
-            if (r + 4 <= p.rows) {
+        for (int k = 0; k < 8; ++k, out += p.ldqt) {
+            if (k >= cols) break;
+            const uint32_t b = tq[L::spot(warp * 8 + k, lane)];
+            if (whole) {
                 *reinterpret_cast<uint32_t*>(out) = b;
             } else {
                 for (int e = 0; e < 4; ++e)
