@@ -88,7 +88,8 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 // Split  128 columns, one tile per cluster, for calls with few tiles (few rows, or a
 //        weight's gradient): the CTAs of the cluster each sum a run of blocks and join
 //        their fp32 results through distributed shared memory in rank order -- the same
-//        bits on every run, one launch, no workspace.
+//        bits on every run, one launch, no workspace.  The summing warps work in two
+//        groups on alternate blocks, so that each waits half as often.
 //
 // The summing warps are what bounds the long sums: a block's 128 x BN results are read
 // from TMEM and added in the time the tensor core takes for the next (512 cycles at BN =
@@ -104,7 +105,10 @@ template <int BN_, int STAGES_, bool JOIN_>
 struct Config {
     static constexpr int BN = BN_, STAGES = STAGES_;
     static constexpr bool JOIN = JOIN_;                    // a cluster's CTAs join one tile
-    static constexpr int COLS = 4 * BN / SUM_WARPS;        // columns a summing warp holds
+    static constexpr int GROUPS = JOIN ? 2 : 1;            // groups of summing warps, which take the blocks in turn
+    static constexpr int GROUP_WARPS = SUM_WARPS / GROUPS;
+    static constexpr int COLS = 4 * BN / GROUP_WARPS;      // columns a summing warp holds
+    static constexpr int BUFS = 512 / BN;                  // blocks' results in TMEM
     static constexpr int STAGE_BYTES = (BM + BN) * BK;
     static constexpr int SLOT = (BM + BN) * 4;             // 128 scales of x, then BN / 128 or BN of w
     static constexpr int BOX = 32 * 128;                   // JOIN: the tile lies over the stages instead
@@ -112,11 +116,11 @@ struct Config {
     static constexpr int ring_off = stg_off + (JOIN ? 0 : SUM_WARPS * BOX);
     static constexpr int bias_off = ring_off + RING * SLOT;
     static constexpr int bar_off = bias_off + 2 * BN * 4;
-    static constexpr int n_bars = 2 * STAGES + 2 * RING + 9;
+    static constexpr int n_bars = 2 * STAGES + 2 * RING + 2 * BUFS + 5;
     static constexpr int misc_off = bar_off + n_bars * 8;
     static constexpr int smem = misc_off + 16 + 1024;
     static_assert(smem <= 232448, "shared memory budget");
-    static_assert(!JOIN || (BN == 128 && stg_off >= BM * BN * 4), "the joined tile lies over the stages");
+    static_assert(!JOIN || (BN == 128 && stg_off >= GROUPS * BM * BN * 4), "the groups' tiles lie over the stages");
 };
 using Wide = Config<256, 3, false>;
 using Split = Config<128, 6, true>;
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
-    constexpr int BN = L::BN, COLS = L::COLS, STAGES = L::STAGES;
+    constexpr int BN = L::BN, COLS = L::COLS, STAGES = L::STAGES, BUFS = L::BUFS;
     // through a shuffle, so that the compiler knows it is the same for the warp (uniform registers)
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int tn = (p.N + BN - 1) / BN, tiles = (p.M + BM - 1) / BM * tn;
@@ -162,10 +166,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto bar_sfull = [&](uint32_t i) { return bar(2 * STAGES + i); };
     auto bar_sempty = [&](uint32_t i) { return bar(2 * STAGES + RING + i); };
     auto bar_accf = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + b); };
-    auto bar_acce = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 2 + b); };
-    auto bar_bfull = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 4 + b); };
-    auto bar_bempty = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 6 + b); };
-    const uint32_t bar_done = bar(2 * STAGES + 2 * RING + 8);
+    auto bar_acce = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + BUFS + b); };
+    auto bar_bfull = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 2 * BUFS + b); };
+    auto bar_bempty = [&](uint32_t b) { return bar(2 * STAGES + 2 * RING + 2 * BUFS + 2 + b); };
+    const uint32_t bar_done = bar(2 * STAGES + 2 * RING + 2 * BUFS + 4);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + L::misc_off);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::misc_off + 4);
 
@@ -176,11 +180,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < RING; ++i) {
             mbar_init(bar_sfull(i), 32);
-            mbar_init(bar_sempty(i), SUM_WARPS);
+            mbar_init(bar_sempty(i), L::GROUP_WARPS);
+        }
+        for (int b = 0; b < BUFS; ++b) {
+            mbar_init(bar_accf(b), 1);
+            mbar_init(bar_acce(b), L::GROUP_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(bar_accf(b), 1);
-            mbar_init(bar_acce(b), SUM_WARPS);
             mbar_init(bar_bfull(b), 32);
             mbar_init(bar_bempty(b), SUM_WARPS);
         }
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_barrier_init();
     }
     if (warp == 0) {
-        tmem_alloc(base + L::misc_off, 2 * BN);
+        tmem_alloc(base + L::misc_off, BUFS * BN);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -224,8 +230,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr uint32_t IDESC = idesc_e4m3(BM, BN);
             for (int t = t0; ok && t < tiles; t += step) {
                 for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                    const uint32_t st = n % STAGES, b = n & 1;
-                    ok = mbar_wait(bar_acce(b), ((n >> 1) & 1) ^ 1, abort_flag, kLinTimeout | 0x13);
+                    const uint32_t st = n % STAGES, b = n % BUFS;
+                    ok = mbar_wait(bar_acce(b), ((n / BUFS) & 1) ^ 1, abort_flag, kLinTimeout | 0x13);
                     if (ok) ok = mbar_wait(bar_full(st), (n / STAGES) & 1, abort_flag, kLinTimeout | 0x14);
                     if (!ok) break;
                     tc_fence_after();
@@ -281,24 +287,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         regs_increase<SUM_REGS>();
-        const int quarter = warp & 3, col_w = ((warp - 4) >> 2) * COLS;   // this warp's lanes and columns of the tile
+        // this warp's lanes and columns of the tile, and its group
+        const int quarter = warp & 3, col_w = ((warp - 4) % L::GROUP_WARPS >> 2) * COLS, group = (warp - 4) / L::GROUP_WARPS;
         const uint32_t box = base + L::stg_off + (uint32_t)(warp - 4) * L::BOX;
         if (!L::JOIN && lane == 0) prefetch_tmap(&tm_y);
         bool ok = true;
-        uint32_t n = 0, tile_no = 0;
+        uint32_t n = (uint32_t)group, tile_no = 0;
         for (int t = t0; ok && t < tiles; t += step, ++tile_no) {
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
             const bool live = !L::JOIN || t / tn * BM + 32 * quarter < p.M;   // else no row of y: only arrivals
 #pragma unroll 1
-            for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                const uint32_t b = n & 1, rs = n % RING;
+            for (int kb = kb0 + group; kb < kb1; kb += L::GROUPS, n += L::GROUPS) {
+                const uint32_t b = n % BUFS, rs = n % RING;
                 ok = mbar_wait(bar_sfull(rs), (n / RING) & 1, abort_flag, kLinTimeout | 0x19);
                 const float* ring = reinterpret_cast<const float*>(gbase + L::ring_off + rs * L::SLOT);
                 float f = ring[32 * quarter + lane];
                 if (!SW_ROWS) f *= ring[BM + col_w / 128];
-                if (ok) ok = mbar_wait(bar_accf(b), (n >> 1) & 1, abort_flag, kLinTimeout | 0x16);
+                if (ok) ok = mbar_wait(bar_accf(b), (n / BUFS) & 1, abort_flag, kLinTimeout | 0x16);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -339,13 +346,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (!ok) break;
             if constexpr (L::JOIN) {
-                // the last block's results are there, so every load has landed and every MMA is
-                // done: the stages take the fp32 tile
+                // once every MMA is done every load has been used too: the stages take the fp32 tile,
+                // one of each group
+                ok = mbar_wait(bar_done, 0, abort_flag, kLinTimeout | 0x1b);
+                ok = __all_sync(0xffffffffu, ok);
                 const int row = 32 * quarter + lane;
-                if (t / tn * BM + row < p.M) {
+                if (ok && t / tn * BM + row < p.M) {
 #pragma unroll
                     for (int i = 0; i < COLS / 4; ++i)
-                        sts128(tile_addr(base, row, col_w / 4 + i), __float_as_uint(f2lo(acc[2 * i])),
+                        sts128(tile_addr(base + (uint32_t)(group * BM * BN * 4), row, col_w / 4 + i), __float_as_uint(f2lo(acc[2 * i])),
                                __float_as_uint(f2hi(acc[2 * i])), __float_as_uint(f2lo(acc[2 * i + 1])),
                                __float_as_uint(f2hi(acc[2 * i + 1])));
                 }
@@ -452,8 +461,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (c >= p.N) continue;
             const uint32_t at = tile_addr(base, r, ch);
             float o[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int k = 0; k < S; ++k) {
-                const float4 v = ld_cluster(at, (uint32_t)k);
+            for (int k = 0; k < L::GROUPS * S; ++k) {
+                const float4 v = ld_cluster(at + (uint32_t)(k % L::GROUPS * BM * BN * 4), (uint32_t)(k / L::GROUPS));
                 o[0] += v.x;
                 o[1] += v.y;
                 o[2] += v.z;
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * BN);
+        tmem_dealloc(tmem, BUFS * BN);
     }
 }
 
