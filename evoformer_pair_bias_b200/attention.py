@@ -36,7 +36,8 @@ EXPORTS = ("evo_attn_fwd", "evo_attn_bwd", "evo_attn_bwd_workspace_bytes", "evo_
            "evo_attn_timing_enable", "evo_attn_timing_collect", "evo_ln_linear", "evo_ln_pair_bias",
            "evo_tri_mul", "evo_outer_product_mean", "evo_sum_partials", "evo_attn_set_wait_limit_ns",
            "evo_exp2_fma", "evo_add_rms_norm_fp8", "evo_add_rms_norm_bwd", "evo_add_rms_norm_bwd_workspace_bytes",
-           "evo_quantize_fp8", "evo_quantize_fp8_both", "evo_fp8_linear")
+           "evo_quantize_fp8", "evo_quantize_fp8_both", "evo_fp8_linear",
+           "evo_fp8_linear_workspace_bytes")
 
 #: Default limit of the kernels' bounded waits (EVO_WAIT_LIMIT_NS), nanoseconds.
 DEFAULT_WAIT_LIMIT_NS = 2_000_000_000
@@ -131,8 +132,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.evo_quantize_fp8_both.argtypes = [i64, i64, ci, vp, i64, ci, vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp]
     lib.evo_quantize_fp8_both.restype = ci
     lib.evo_fp8_linear.argtypes = [i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, ci, vp, ci, vp, i64,
-                                   vp]
+                                   vp, ctypes.c_size_t, vp]
     lib.evo_fp8_linear.restype = ci
+    lib.evo_fp8_linear_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.evo_fp8_linear_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib
     return lib
 

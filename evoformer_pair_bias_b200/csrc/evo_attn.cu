@@ -513,15 +513,17 @@ evo_status_t launch_linear_as(const evo::fp8::LinParams& p, int S, cudaStream_t 
         return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
     }();
     if (regs != f8::LAUNCH_REGS) return EVO_ERR_CUDA;
-    const int64_t tiles = (int64_t)((p.M + f8::BM - 1) / f8::BM) * ((p.N + L::BN - 1) / L::BN);
+    const int64_t tm = (p.M + f8::BM - 1) / f8::BM;
+    const int64_t tiles = tm * ((p.N + L::BN - 1) / L::BN) * (L::PART ? p.parts : 1);
     if (tiles * S > 0x7fffffff - 65536) return EVO_ERR_UNSUPPORTED;
+    const int64_t y_rows = L::PART ? tm * f8::BM * p.parts : p.M;
     const int64_t e = sizeof(T);
     const bool tma_out = !L::JOIN && aligned(p.y, 16) && (p.M == 1 || p.ldy * e % 16 == 0);
     CUtensorMap maps[3];
     std::memset(maps, 0, sizeof(maps));
     if (!evo::tma::matrix_u8(&maps[0], p.x, p.M, p.K, p.ldx, f8::BM) ||
         !evo::tma::matrix_u8(&maps[1], p.w, p.N, p.K, p.ldw, L::BN) ||
-        (tma_out && !evo::tma::boxes_out(&maps[2], p.y, p.M, p.N, p.ldy, (int)e)))
+        (tma_out && !evo::tma::boxes_out(&maps[2], p.y, y_rows, p.N, p.ldy, (int)e)))
         return EVO_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(L::JOIN ? tiles * S : std::min<int64_t>(tiles, sm_count())));
@@ -539,58 +541,60 @@ evo_status_t launch_linear_as(const evo::fp8::LinParams& p, int S, cudaStream_t 
     return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
 
-// CTAs of the split kernel that join a tile, 1 to 8: the number whose clusters finish first.  A
-// cluster's CTAs have to lie in one GPC, so the count that run at once is asked for (of 148 SMs:
-// 74 clusters of 2, 33 of 4, 22 of 6, 15 of 8); the answers are kept per device.  Each CTA
-// is left at least two blocks.
-template <typename T, bool SW_ROWS>
-int split_of(int64_t tiles, int64_t blocks) {
+// Which form a product takes: Wide (S = 1), Split with S CTAs a tile, or Parts with S runs a tile.
+struct LinPlan {
+    enum Form { WIDE, SPLIT, PARTS } form;
+    int S;
+    size_t workspace;            // bytes
+    int64_t ld;                  // Parts: pitch of the workspace's rows
+};
+// A pure function of the sizes.  The costs are in blocks of 128 x 256 x 128 on one SM (0.6 us):
+// a block of 128 columns takes as long as one of 256 (both wait more than they add), a CTA's start,
+// last step and end about five, a second launch with its pass over the parts four more.  Measured
+// both ways: 1024 x 131072 x 256 takes 99 us in clusters of 6, TODO in parts; 300 x 512 x 2048
+// TODO in clusters of 2, TODO in parts.
+LinPlan plan_linear(int64_t M, int64_t N, int64_t K) {
     namespace f8 = evo::fp8;
-    static std::atomic<int> at_once[256][9];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return 1;
-    int best = 1;
-    double best_t = 0;
+    // clusters of 1 to 8 CTAs that run at once on 148 SMs (a cluster lies in one GPC)
+    static const int at_once[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+    const int64_t tm = (M + f8::BM - 1) / f8::BM, blocks = (K + f8::BK - 1) / f8::BK;
+    const int64_t wide = tm * ((N + 255) / 256), narrow = tm * ((N + 127) / 128);
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    LinPlan best{LinPlan::WIDE, 1, 0, 0};
+    int64_t t_best = up(wide, 148) * (blocks + 5);
+    if (narrow > 148) return best;
     for (int S = 1; S <= 8 && (S == 1 || blocks >= 2 * S); ++S) {
-        int n = at_once[dev][S].load();
-        if (n == 0) {
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3((unsigned)S);
-            cfg.blockDim = dim3(f8::THREADS);
-            cfg.dynamicSmemBytes = f8::Split::smem;
-            cudaLaunchAttribute attr{};
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = (unsigned)S;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&n, f8::linear_kernel<T, SW_ROWS, f8::Split>, &cfg) != cudaSuccess || n < 1) {
-                (void)cudaGetLastError();
-                n = -1;
-            }
-            at_once[dev][S].store(n);
+        const int64_t t = up(narrow, at_once[S]) * (up(blocks, S) + 5);
+        if (t < t_best) {
+            t_best = t;
+            best = {LinPlan::SPLIT, S, 0, 0};
         }
-        if (n < 1) continue;
-        // a CTA's start, join and end cost about as much as six blocks
-        const double t = (double)((tiles + n - 1) / n) * (double)((blocks + S - 1) / S + 6);
-        if (best_t == 0 || t < best_t) {
-            best = S;
-            best_t = t;
-        }
+    }
+    const int64_t S = std::min<int64_t>(148 / std::max<int64_t>(wide, 1), blocks / 2);
+    if (S > 1 && up(blocks, S) + 9 < t_best) {
+        const int64_t ld = up(N, 4) * 4;
+        best = {LinPlan::PARTS, (int)S, (size_t)(S * tm * f8::BM * ld) * sizeof(float), ld};
     }
     return best;
 }
 
 template <typename T, bool SW_ROWS>
-evo_status_t launch_linear(const evo::fp8::LinParams& p, cudaStream_t stream) {
+evo_status_t launch_linear(const evo::fp8::LinParams& p, const LinPlan& plan, void* workspace, cudaStream_t stream) {
     namespace f8 = evo::fp8;
-    const int64_t blocks = (p.K + f8::BK - 1) / f8::BK;
-    const int64_t tiles = (int64_t)((p.M + f8::BM - 1) / f8::BM) * ((p.N + f8::Split::BN - 1) / f8::Split::BN);
-    if (tiles > sm_count()) return launch_linear_as<T, SW_ROWS, f8::Wide>(p, 1, stream);
-    static std::atomic<uint64_t> granted[4];               // the occupancy query wants it first
-    if (!grant_smem(f8::linear_kernel<T, SW_ROWS, f8::Split>, f8::Split::smem, granted)) return EVO_ERR_CUDA;
-    const int S = split_of<T, SW_ROWS>(tiles, blocks);
-    return launch_linear_as<T, SW_ROWS, f8::Split>(p, S, stream);
+    if (plan.form == LinPlan::WIDE) return launch_linear_as<T, SW_ROWS, f8::Wide>(p, 1, stream);
+    if (plan.form == LinPlan::SPLIT) return launch_linear_as<T, SW_ROWS, f8::Split>(p, plan.S, stream);
+    f8::LinParams parts = p;
+    parts.y = workspace;
+    parts.ldy = plan.ld;
+    parts.bias = nullptr;
+    parts.parts = plan.S;
+    const evo_status_t st = launch_linear_as<float, SW_ROWS, f8::Parts>(parts, 1, stream);
+    if (st != EVO_OK) return st;
+    const int64_t items = (int64_t)p.M * ((p.N + 3) / 4), rows = (int64_t)(p.M + f8::BM - 1) / f8::BM * f8::BM;
+    const int grid = (int)std::min<int64_t>((items + 255) / 256, 148 * 8);
+    f8::sum_parts_kernel<T><<<grid, 256, 0, stream>>>(static_cast<const float*>(workspace), plan.ld, rows, plan.S, p);
+    g_launches += 1;
+    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
 
 }  // namespace
@@ -1035,10 +1039,16 @@ evo_status_t evo_quantize_fp8_both(int64_t rows, int64_t cols, evo_dtype_t dtype
     return quantize(p, dtype, square != 0, static_cast<cudaStream_t>(stream));
 }
 
+size_t evo_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    const int64_t most = (int64_t)0x7fffffff - 256;
+    return M < 1 || N < 1 || K < 1 || M > most || N > most || K > most ? 0 : plan_linear(M, N, K).workspace;
+}
+
 evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const float* x_scale,
                             int64_t x_scale_row, int64_t x_scale_group, const void* w, int64_t ldw,
                             const float* w_scale, int64_t w_scale_row, int64_t w_scale_group, int w_scale_rows,
-                            const float* bias, evo_dtype_t y_dtype, void* y, int64_t ldy, void* stream) {
+                            const float* bias, evo_dtype_t y_dtype, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, void* stream) {
     if (M < 0 || N < 0 || K < 1 || !dtype_ok(y_dtype)) return EVO_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return EVO_OK;
     if (!x || !x_scale || !w || !w_scale || !y) return EVO_ERR_INVALID_ARG;
@@ -1050,6 +1060,9 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
         return EVO_ERR_UNSUPPORTED;
     const int64_t most = (int64_t)0x7fffffff - 256;
     if (M > most || N > most || K > most) return EVO_ERR_UNSUPPORTED;
+    const LinPlan plan = plan_linear(M, N, K);
+    if (plan.workspace > 0 && (!workspace || workspace_bytes < plan.workspace)) return EVO_ERR_WORKSPACE_TOO_SMALL;
+    if (plan.workspace > 0 && !aligned(workspace, 256)) return EVO_ERR_INVALID_ARG;
     evo::fp8::LinParams p{};
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
     p.x = x; p.ldx = ldx; p.w = w; p.ldw = ldw;
@@ -1058,8 +1071,8 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
     p.bias = bias; p.y = y; p.ldy = ldy;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (y_dtype == EVO_DTYPE_BF16)
-        return w_scale_rows ? launch_linear<__nv_bfloat16, true>(p, s) : launch_linear<__nv_bfloat16, false>(p, s);
-    return w_scale_rows ? launch_linear<float, true>(p, s) : launch_linear<float, false>(p, s);
+        return w_scale_rows ? launch_linear<__nv_bfloat16, true>(p, plan, workspace, s) : launch_linear<__nv_bfloat16, false>(p, plan, workspace, s);
+    return w_scale_rows ? launch_linear<float, true>(p, plan, workspace, s) : launch_linear<float, false>(p, plan, workspace, s);
 }
 
 }  // extern "C"

@@ -37,6 +37,7 @@ struct LinParams {
     const float* bias;             // [N] or null
     void* y;                       // bf16 or fp32 [M, N]
     int64_t ldy;
+    int parts;                     // Parts: runs of blocks; y is then fp32 [parts * (M up to whole tiles), N]
 };
 
 // kind::f8f6f4, e4m3 x e4m3 -> fp32, both operands K-major.
@@ -90,6 +91,9 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 //        their fp32 results through distributed shared memory in rank order -- the same
 //        bits on every run, one launch, no workspace.  The summing warps work in two
 //        groups on alternate blocks, so that each waits half as often.
+// Parts  256 columns, for long sums into few tiles: items of a tile and a run of blocks fill
+//        the GPU whatever the number of tiles is (clusters of 8 leave a quarter of it idle),
+//        and their fp32 results go to a workspace, which sum_parts_kernel adds in order.
 //
 // The summing warps are what bounds the long sums: a block's 128 x BN results are read
 // from TMEM and added in the time the tensor core takes for the next (512 cycles at BN =
@@ -101,10 +105,12 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 constexpr int SUM_WARPS = 16;                              // 4 column groups x 4 lane quarters
 constexpr int THREADS = 32 * (4 + SUM_WARPS);
 constexpr int RING = 8;                                    // blocks whose scales are held
-template <int BN_, int STAGES_, bool JOIN_>
+enum Mode { WHOLE, JOINED, PARTS };
+template <int BN_, int STAGES_, Mode MODE>
 struct Config {
     static constexpr int BN = BN_, STAGES = STAGES_;
-    static constexpr bool JOIN = JOIN_;                    // a cluster's CTAs join one tile
+    static constexpr bool JOIN = MODE == JOINED;           // a cluster's CTAs join one tile
+    static constexpr bool PART = MODE == PARTS;            // each item sums a run of blocks into the workspace
     static constexpr int GROUPS = JOIN ? 2 : 1;            // groups of summing warps, which take the blocks in turn
     static constexpr int GROUP_WARPS = SUM_WARPS / GROUPS;
     static constexpr int COLS = 4 * BN / GROUP_WARPS;      // columns a summing warp holds
@@ -122,8 +128,9 @@ struct Config {
     static_assert(smem <= 232448, "shared memory budget");
     static_assert(!JOIN || (BN == 128 && stg_off >= GROUPS * BM * BN * 4), "the groups' tiles lie over the stages");
 };
-using Wide = Config<256, 3, false>;
-using Split = Config<128, 6, true>;
+using Wide = Config<256, 3, WHOLE>;
+using Split = Config<128, 6, JOINED>;
+using Parts = Config<256, 3, PARTS>;
 // registers per thread: 96 at launch (20 warps), handed from the control warps to the others
 constexpr int LAUNCH_REGS = 96, CTRL_REGS = 32, SUM_REGS = 112;
 static_assert(4 * CTRL_REGS + SUM_WARPS * SUM_REGS <= (4 + SUM_WARPS) * LAUNCH_REGS, "register split");
@@ -159,7 +166,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     // this CTA's tiles t0, t0 + step, ... and of each the blocks kb0 .. kb1 - 1
     const int S = L::JOIN ? (int)cluster_size() : 1, rank = L::JOIN ? (int)cluster_rank() : 0;
     const int t0 = (int)blockIdx.x / S, step = L::JOIN ? tiles : (int)gridDim.x;
-    const int kb0 = (int)((int64_t)all_kb * rank / S), kb1 = (int)((int64_t)all_kb * (rank + 1) / S);
+    const int kb0_c = (int)((int64_t)all_kb * rank / S), kb1_c = (int)((int64_t)all_kb * (rank + 1) / S);
+    // Parts: item t is part t % parts of tile t / parts
+    const int parts = L::PART ? p.parts : 1, items = tiles * parts;
+    auto first_kb = [&](int t) { return L::PART ? (int)((int64_t)all_kb * (t % parts) / parts) : kb0_c; };
+    auto end_kb = [&](int t) { return L::PART ? (int)((int64_t)all_kb * (t % parts + 1) / parts) : kb1_c; };
     auto bar = [&](int i) { return base + L::bar_off + 8u * i; };
     auto bar_full = [&](uint32_t i) { return bar(i); };
     auto bar_empty = [&](uint32_t i) { return bar(STAGES + i); };
@@ -210,8 +221,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 0 && lane == 0) {
             prefetch_tmap(&tm_x);
             prefetch_tmap(&tm_w);
-            for (int t = t0; ok && t < tiles; t += step) {
-                const int m0 = t / tn * BM, n0 = t % tn * BN;
+            for (int t = t0; ok && t < items; t += step) {
+                const int tile = t / parts, m0 = tile / tn * BM, n0 = tile % tn * BN, kb0 = first_kb(t), kb1 = end_kb(t);
                 for (int kb = kb0; ok && kb < kb1; ++kb, ++n) {
                     const uint32_t st = n % STAGES;
                     ok = mbar_wait(bar_empty(st), ((n / STAGES) & 1) ^ 1, abort_flag, kLinTimeout | 0x11);
@@ -228,7 +239,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_wait(bar_full(u % STAGES), (u / STAGES) & 1, &no_abort, kLinTimeout | 0x12);
         } else if (warp == 1 && lane == 0) {
             constexpr uint32_t IDESC = idesc_e4m3(BM, BN);
-            for (int t = t0; ok && t < tiles; t += step) {
+            for (int t = t0; ok && t < items; t += step) {
+                const int kb0 = first_kb(t), kb1 = end_kb(t);
                 for (int kb = kb0; kb < kb1; ++kb, ++n) {
                     const uint32_t st = n % STAGES, b = n % BUFS;
                     ok = mbar_wait(bar_acce(b), ((n / BUFS) & 1) ^ 1, abort_flag, kLinTimeout | 0x13);
@@ -249,8 +261,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_wait(bar_done, 0, &no_abort, kLinTimeout | 0x15);
         } else if (warp == 2) {
             constexpr int WS = SW_ROWS ? BN / 32 : 1;            // scales of w a lane fetches
-            for (int t = t0; ok && t < tiles; t += step) {
-                const int m0 = t / tn * BM, n0 = t % tn * BN;
+            for (int t = t0; ok && t < items; t += step) {
+                const int tile = t / parts, m0 = tile / tn * BM, n0 = tile % tn * BN, kb0 = first_kb(t), kb1 = end_kb(t);
                 const float *fx[4], *fw[WS];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) fx[i] = p.sx + (int64_t)min(m0 + lane + 32 * i, p.M - 1) * p.sx_row;
@@ -273,8 +285,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             cp_async_wait_all();
         } else if (warp == 3 && p.bias && !L::JOIN) {
-            for (int t = t0; ok && t < tiles; t += step, ++n) {
-                const int n0 = t % tn * BN;
+            for (int t = t0; ok && t < items; t += step, ++n) {
+                const int n0 = t / parts % tn * BN;
                 const uint32_t b = n & 1, dst = base + L::bias_off + b * BN * 4 + 4 * lane;
                 ok = mbar_wait(bar_bempty(b), ((n >> 1) & 1) ^ 1, abort_flag, kLinTimeout | 0x18);
                 ok = __all_sync(0xffffffffu, ok);
@@ -293,11 +305,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!L::JOIN && lane == 0) prefetch_tmap(&tm_y);
         bool ok = true;
         uint32_t n = (uint32_t)group, tile_no = 0;
-        for (int t = t0; ok && t < tiles; t += step, ++tile_no) {
+        for (int t = t0; ok && t < items; t += step, ++tile_no) {
             uint64_t acc[COLS / 2];
 #pragma unroll
             for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
-            const bool live = !L::JOIN || t / tn * BM + 32 * quarter < p.M;   // else no row of y: only arrivals
+            const int tile = t / parts, kb0 = first_kb(t), kb1 = end_kb(t);
+            const bool live = (!L::JOIN && !L::PART) || tile / tn * BM + 32 * quarter < p.M;   // else no row of y: only arrivals
 #pragma unroll 1
             for (int kb = kb0 + group; kb < kb1; kb += L::GROUPS, n += L::GROUPS) {
                 const uint32_t b = n % BUFS, rs = n % RING;
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ok = mbar_wait(bar_done, 0, abort_flag, kLinTimeout | 0x1b);
                 ok = __all_sync(0xffffffffu, ok);
                 const int row = 32 * quarter + lane;
-                if (ok && t / tn * BM + row < p.M) {
+                if (ok && tile / tn * BM + row < p.M) {
 #pragma unroll
                     for (int i = 0; i < COLS / 4; ++i)
                         sts128(tile_addr(base + (uint32_t)(group * BM * BN * 4), row, col_w / 4 + i), __float_as_uint(f2lo(acc[2 * i])),
@@ -362,7 +375,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // ------------------------------------------------ the tile leaves
             constexpr int CPB = 128 / sizeof(T);           // columns a box
-            const int row0 = t / tn * BM + 32 * quarter, col0 = t % tn * BN + col_w;
+            const int row0 = tile / tn * BM + 32 * quarter, col0 = tile % tn * BN + col_w;
+            const int out0 = L::PART ? t % parts * ((p.M + BM - 1) / BM * BM) + row0 : row0;   // the row of y that row0 becomes
             const float* bias_s = reinterpret_cast<const float*>(gbase + L::bias_off) + (tile_no & 1) * BN + col_w;
             if (p.bias) {
                 ok = mbar_wait(bar_bfull(tile_no & 1), (tile_no >> 1) & 1, abort_flag, kLinTimeout | 0x1a);
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && row0 < p.M && c0 < p.N) {
-                        tma_store_2d(&tm_y, box, c0, row0);
+                        tma_store_2d(&tm_y, box, c0, out0);
                         bulk_commit();
                     }
                 } else {
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         uint32_t v;
                         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(place(r, w >> 2) + (w & 3) * 4));
                         const uint32_t next = __shfl_down_sync(0xffffffffu, v, 1);
-                        T* out = static_cast<T*>(p.y) + (int64_t)(row0 + r) * p.ldy + c0;
+                        T* out = static_cast<T*>(p.y) + (int64_t)(out0 + r) * p.ldy + c0;
                         if constexpr (sizeof(T) == 4) {
                             if (c0 + w < p.N) out[w] = __uint_as_float(v);
                         } else {
@@ -495,6 +509,45 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, BUFS * BN);
+    }
+}
+
+// y = the parts of Parts, added in order, + bias.  One thread per four columns; the parts were
+// written just before and lie in L2.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* part, int64_t ld, int64_t part_rows, int parts,
+                                                        const LinParams p) {
+    const int64_t per_row = (p.N + 3) / 4, items = p.M * per_row;
+    const bool vec = (p.M == 1 || p.ldy % 4 == 0) && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < items; t += (int64_t)gridDim.x * 256) {
+        const int64_t r = t / per_row, c = (t - r * per_row) * 4;
+        const float* at = part + r * ld + c;
+        float4 o = *reinterpret_cast<const float4*>(at);
+#pragma unroll 8
+        for (int k = 1; k < parts; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(at + k * part_rows * ld);
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+        }
+        float f[4] = {o.x, o.y, o.z, o.w};
+        if (p.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.N) f[e] += __ldg(p.bias + c + e);
+        }
+        T* out = static_cast<T*>(p.y) + r * p.ldy + c;
+        if (vec && c + 4 <= p.N) {
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+            else
+                *reinterpret_cast<float4*>(out) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.N) Elem<T>::store(out + e, f[e]);
+        }
     }
 }
 

@@ -286,8 +286,11 @@ def fp8_linear(xq, x_scale, wq, w_scale, bias=None, out_dtype=torch.bfloat16):
     y = _empty((M, N), (N, 1), dtype=out_dtype, device=dev)
     if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
         bias = _opt_f32(bias, N, dev)
+    nbytes, ws = load_library().evo_fp8_linear_workspace_bytes(M, N, K), None
+    if nbytes:
+        ws = _empty((nbytes // 4,), (1,), dtype=torch.float32, device=dev)
     _call("evo_fp8_linear", dev, M, N, K, x_at, ldx, xs.data_ptr(), sxr, sxg, w_at, ldw, w_scale.data_ptr(), swr, swg,
-          sn != blocks, _addr(bias), DTYPES[out_dtype], y.data_ptr(), N)
+          sn != blocks, _addr(bias), DTYPES[out_dtype], y.data_ptr(), N, _addr(ws), nbytes)
     return y if len(lead) == 1 else y.view(*lead, N)
 
 

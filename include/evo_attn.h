@@ -411,15 +411,20 @@ evo_status_t evo_quantize_fp8_both(int64_t rows, int64_t cols, evo_dtype_t dtype
  * (w_scale_rows != 0: both operands of a weight's gradient).  Each block's
  * product is summed by the tensor cores in fp32, the blocks by fp32
  * fused multiply-adds; bias: fp32 [N] or NULL; y: y_dtype [M, N], row pitch
- * ldy (elements); only [0:M, 0:N] is written.  The sum's order is fixed: the
- * same bits on every run.  K >= 1; M == 0 or N == 0 is a no-op.  Waits in the
+ * ldy (elements); only [0:M, 0:N] is written.  The sum's order is fixed by
+ * the sizes: the same bits on every run.  workspace: device buffer of at least
+ * evo_fp8_linear_workspace_bytes(M, N, K) bytes (0 for most sizes: then it may
+ * be NULL), 256-byte aligned, contents arbitrary; calls that may overlap need
+ * one each.  K >= 1; M == 0 or N == 0 is a no-op.  Waits in the
  * kernel are bounded, and one that gives up is reported by
  * evo_attn_device_status.
  */
+size_t evo_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const float* x_scale,
                             int64_t x_scale_row, int64_t x_scale_group, const void* w, int64_t ldw,
                             const float* w_scale, int64_t w_scale_row, int64_t w_scale_group, int w_scale_rows,
-                            const float* bias, evo_dtype_t y_dtype, void* y, int64_t ldy, void* stream);
+                            const float* bias, evo_dtype_t y_dtype, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* evo_status_string(evo_status_t status);

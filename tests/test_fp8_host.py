@@ -98,8 +98,9 @@ def test_norm_bwd_refusals_and_workspace(lib):
 
 
 def test_linear_refusals(lib):
-    def f(M=8, N=8, K=64, x=FAKE, ldx=64, xs=FAKE, w=FAKE, ldw=64, ws=FAKE, bias=NUL, yd=0, y=FAKE, ldy=8, sxr=1):
-        return lib.evo_fp8_linear(M, N, K, x, ldx, xs, sxr, 8, w, ldw, ws, 1, 1, 0, bias, yd, y, ldy, NUL)
+    def f(M=8, N=8, K=64, x=FAKE, ldx=64, xs=FAKE, w=FAKE, ldw=64, ws=FAKE, bias=NUL, yd=0, y=FAKE, ldy=8, sxr=1,
+          work=NUL, nb=0):
+        return lib.evo_fp8_linear(M, N, K, x, ldx, xs, sxr, 8, w, ldw, ws, 1, 1, 0, bias, yd, y, ldy, work, nb, NUL)
     assert f(M=0, x=NUL, y=NUL) == 0 and f(N=0, w=NUL) == 0
     assert f(M=-1) == 1 and f(K=0) == 1 and f(yd=3) == 1
     assert f(x=NUL) == 1 and f(xs=NUL) == 1 and f(w=NUL) == 1 and f(ws=NUL) == 1 and f(y=NUL) == 1
@@ -107,6 +108,16 @@ def test_linear_refusals(lib):
     assert f(ldx=72) == 2 and f(ldw=72) == 2 and f(x=ODD4) == 2 and f(w=ODD4) == 2
     assert f(M=1 << 31) == 2 and f(N=1 << 31, ldy=1 << 31) == 2 and f(K=1 << 31, ldx=1 << 31, ldw=1 << 31) == 2
     assert f(xs=ODD) == 1 and f(bias=ODD) == 1 and f(yd=1, y=ODD) == 1
+    need = lib.evo_fp8_linear_workspace_bytes
+    assert need(0, 8, 8) == 0 and need(8, 8, 0) == 0 and need(8, 8, 1 << 40) == 0 and need(8, 8, 64) == 0
+    assert need(131072, 1024, 256) == 0 and need(8192, 8192, 1 << 20) == 0        # tiles enough
+    big = need(1024, 256, 131072)                                                  # few tiles, a long sum: parts
+    assert 0 < big <= 64 << 20 and big == need(1024, 256, 131072)
+    long = dict(M=1024, N=256, K=131072, ldx=131072, ldw=131072, ldy=256)
+    assert f(**long) == 3 and f(work=FAKE, nb=big - 1, **long) == 3
+    assert f(work=ctypes.c_void_p((1 << 20) + 16), nb=big, **long) == 1
+    for M, N, K in ((1, 8192, 8192), (3, 77, 1 << 20), (129, 257, 70001), (1, 1, 1 << 30)):
+        assert need(M, N, K) <= 148 * 128 * 256 * 4 + (1 << 22)                   # bounded by the GPU, not by K
 
 
 def test_binding_refusals():

@@ -333,7 +333,8 @@ def check_linear(y, xq, xs, wq, ws, bias):
 
 SHAPES = [(1, 1, 1), (1, 128, 128), (3, 5, 17), (1, 4096, 4096), (128, 128, 128), (129, 127, 129), (64, 1024, 256),
           (200, 136, 4000), (5, 300, 12345), (257, 1000, 384), (300, 2048, 512), (1, 8, 8192), (17, 777, 1040),
-          (2500, 1024, 256), (700, 1001, 130)]
+          (2500, 1024, 256), (700, 1001, 130),
+          (1, 8192, 8192), (1, 3, 50000), (100, 77, 40001), (129, 257, 16384)]
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
@@ -361,7 +362,9 @@ def test_fp8_linear_large(M, N, K, square):
 def test_fp8_linear_scale_layouts_pitches_and_untouched_bytes():
     g = gen(41)
     lib = A.load_library()
-    for M, N, K in ((130, 200, 300), (70, 129, 128), (520, 264, 1000), (2000, 1024, 256)):
+    work = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    for M, N, K in ((130, 200, 300), (70, 129, 128), (520, 264, 1000), (2000, 1024, 256), (4000, 2056, 130),
+                    (3, 130, 20000), (200, 77, 30000)):
         xq, xs, wq, ws = operands(M, N, K, True, g)
         want = fp8.fp8_linear(xq, xs, wq, ws)
         assert torch.equal(want, fp8.fp8_linear(xq, xs.t().contiguous().t(), wq, ws.t().contiguous().t()))
@@ -374,7 +377,7 @@ def test_fp8_linear_scale_layouts_pitches_and_untouched_bytes():
             buf = torch.full((M + 1, ld), 9.0, dtype=BF16, device="cuda")
             rc = lib.evo_fp8_linear(M, N, K, A._ptr(xq), xq.stride(0), A._ptr(xs), xs.stride(0), xs.stride(1),
                                     A._ptr(wq), wq.stride(0), A._ptr(ws), ws.stride(0), ws.stride(1), 0, None, 0,
-                                    buf.data_ptr() + 2 * off, ld, A._stream(xq.device))
+                                    buf.data_ptr() + 2 * off, ld, A._ptr(work), work.numel(), A._stream(xq.device))
             assert rc == 0
             flat = buf.view(-1)
             y = flat[off:off + M * ld].view(M, ld) if off == 0 else torch.as_strided(flat, (M, N), (ld, 1), off)
