@@ -138,6 +138,9 @@ static_assert(4 * CTRL_REGS + SUM_WARPS * SUM_REGS <= (4 + SUM_WARPS) * LAUNCH_R
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const float* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Arrives on `bar` (which counts the arriving threads) when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -260,26 +263,41 @@ __global__ void __launch_bounds__(THREADS, 1)
             mma_commit(bar_done);
             mbar_wait(bar_done, 0, &no_abort, kLinTimeout | 0x15);
         } else if (warp == 2) {
-            constexpr int WS = SW_ROWS ? BN / 32 : 1;            // scales of w a lane fetches
+            // C scales of the rows from r0 on (the last row again past `rows`), block by block: 16
+            // bytes a copy where the rows' scales lie side by side and aligned (12 single copies a
+            // block held 1024 x 131072 x 256 up: 69 us, 3 wide ones TODO), else one for each row.  The
+            // control warps have 32 registers: a pointer for each copy would spill, and take the
+            // summing warps' code along with it.
+            auto side = [](const float* src, int64_t s_row, int64_t s_grp, int r0, int C, int rows) {
+                return s_row == 1 && s_grp % 4 == 0 && r0 + C <= rows && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+            };
+            auto copy = [&](uint32_t dst, const float* src, bool wide, int r0, int rows, int64_t s_row, auto count) {
+                constexpr int C = decltype(count)::value;
+                if (wide) {
+#pragma unroll
+                    for (int i = 0; i < C / 128; ++i) cp_async16(dst + 16 * lane + 512 * i, src + r0 + 4 * lane + 128 * i);
+                } else {
+#pragma unroll 1
+                    for (int i = lane; i < C; i += 32) cp_async4(dst + 4 * i, src + (int64_t)min(r0 + i, rows - 1) * s_row);
+                }
+            };
             for (int t = t0; ok && t < items; t += step) {
                 const int tile = t / parts, m0 = tile / tn * BM, n0 = tile % tn * BN, kb0 = first_kb(t), kb1 = end_kb(t);
-                const float *fx[4], *fw[WS];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fx[i] = p.sx + (int64_t)min(m0 + lane + 32 * i, p.M - 1) * p.sx_row;
-#pragma unroll
-                for (int i = 0; i < WS; ++i)
-                    fw[i] = p.sw + (int64_t)(SW_ROWS ? min(n0 + lane + 32 * i, p.N - 1)
-                                                     : min(n0 + 128 * (lane & (BN / 128 - 1)), p.N - 1) / 128) * p.sw_row;
-                for (int kb = kb0; kb < kb1; ++kb, ++n) {
-                    const uint32_t st = n % RING, dst = base + L::ring_off + st * L::SLOT + 4 * lane;
+                const bool x_wide = side(p.sx, p.sx_row, p.sx_grp, m0, BM, p.M);
+                const bool w_wide = SW_ROWS && side(p.sw, p.sw_row, p.sw_grp, n0, BN, p.N);
+                const float* sx = p.sx + kb0 * p.sx_grp;
+                const float* sw = p.sw + kb0 * p.sw_grp;
+                if (!SW_ROWS) sw += (int64_t)(min(n0 + 128 * (lane & (BN / 128 - 1)), p.N - 1) / 128) * p.sw_row;
+                for (int kb = kb0; kb < kb1; ++kb, ++n, sx += p.sx_grp, sw += p.sw_grp) {
+                    const uint32_t st = n % RING, dst = base + L::ring_off + st * L::SLOT;
                     ok = mbar_wait(bar_sempty(st), ((n / RING) & 1) ^ 1, abort_flag, kLinTimeout | 0x17);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cp_async4(dst + 128 * i, fx[i] + kb * p.sx_grp);
-#pragma unroll
-                    for (int i = 0; i < WS; ++i)
-                        if (SW_ROWS || lane < BN / 128) cp_async4(dst + 4 * BM + 128 * i, fw[i] + kb * p.sw_grp);
+                    copy(dst, sx, x_wide, m0, p.M, p.sx_row, std::integral_constant<int, BM>{});
+                    if (SW_ROWS)
+                        copy(dst + 4 * BM, sw, w_wide, n0, p.N, p.sw_row, std::integral_constant<int, BN>{});
+                    else if (lane < BN / 128)
+                        cp_async4(dst + 4 * BM + 4 * lane, sw);
                     cp_async_arrive(bar_sfull(st));
                 }
             }
@@ -331,27 +349,45 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     continue;
                 }
+                auto release = [&]() {                     // everything has been read: the buffer is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_acce(b));
+                };
+                if constexpr (SW_ROWS) {
+                    // sixteen columns at a time, their scales (the same for the whole warp) fetched
+                    // before the results, so that one wait covers both
 #pragma unroll
-                for (int c = 0; c < COLS / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32_sync(ta + 32 * c, v);
-                    if (c == COLS / 32 - 1) {              // everything has been read: the buffer is free
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_acce(b));
-                    }
+                    for (int c = 0; c < COLS / 16; ++c) {
+                        uint32_t v[16];
+                        float4 s[4];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        uint64_t t0 = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                        uint64_t t1 = f2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-                        if (SW_ROWS) {
-                            const float4 s = *reinterpret_cast<const float4*>(ring + BM + col_w + 32 * c + i);
-                            t0 = fmul2(t0, f2(s.x, s.y));
-                            t1 = fmul2(t1, f2(s.z, s.w));
+                        for (int i = 0; i < 4; ++i) s[i] = *reinterpret_cast<const float4*>(ring + BM + col_w + 16 * c + 4 * i);
+                        tmem_ld16_sync(ta + 16 * c, v);
+                        if (c == COLS / 16 - 1) release();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const uint64_t t0 = fmul2(f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f2(s[i / 4].x, s[i / 4].y));
+                            const uint64_t t1 = fmul2(f2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), f2(s[i / 4].z, s[i / 4].w));
+                            uint64_t* a = acc + 8 * c + i / 2;
+                            a[0] = ffma2(t0, f2v, a[0]);
+                            a[1] = ffma2(t1, f2v, a[1]);
                         }
-                        uint64_t* a = acc + 16 * c + i / 2;
-                        a[0] = ffma2(t0, f2v, a[0]);
-                        a[1] = ffma2(t1, f2v, a[1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < COLS / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32_sync(ta + 32 * c, v);
+                        if (c == COLS / 32 - 1) release();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const uint64_t t0 = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                            const uint64_t t1 = f2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                            uint64_t* a = acc + 16 * c + i / 2;
+                            a[0] = ffma2(t0, f2v, a[0]);
+                            a[1] = ffma2(t1, f2v, a[1]);
+                        }
                     }
                 }
                 __syncwarp();                              // the slot's scales have been read
