@@ -541,18 +541,19 @@ evo_status_t launch_linear_as(const evo::fp8::LinParams& p, int S, cudaStream_t 
     return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
 
-// Which form a product takes: Wide (S = 1), Split with S CTAs a tile, or Parts with S runs a tile.
+// Which form a product takes: Few with S warps a row of w, Wide (S = 1), Split with S CTAs a tile, or
+// Parts with S runs a tile.
 struct LinPlan {
-    enum Form { WIDE, SPLIT, PARTS } form;
+    enum Form { FEW, WIDE, SPLIT, PARTS } form;
     int S;
     size_t workspace;            // bytes
     int64_t ld;                  // Parts: pitch of the workspace's rows
 };
-// A pure function of the sizes.  The costs are in blocks of 128 x 256 x 128 on one SM (0.6 us):
-// a block of 128 columns takes as long as one of 256 (both wait more than they add), a CTA's start,
-// last step and end about five, a second launch with its pass over the parts four more.  Measured
-// both ways: 1024 x 131072 x 256 takes 99 us in clusters of 6, TODO in parts; 300 x 512 x 2048
-// TODO in clusters of 2, TODO in parts.
+// A pure function of the sizes.  Up to two rows: Few (1 x 8192 x 8192 18.3 us, in parts 22.7; two
+// rows 23.4 and 23.3; four 34.9 and 24).  Else the costs are in blocks of 128 x 256 x 128 on one SM
+// (0.6 us): a block of 128 columns takes as long as one of 256 (both wait more than they add), a
+// CTA's start, last step and end about five, a second launch with its pass over the parts four more.
+// Measured both ways: 1024 x 131072 x 256 takes 99 us in clusters of 6, 60 in parts.
 LinPlan plan_linear(int64_t M, int64_t N, int64_t K) {
     namespace f8 = evo::fp8;
     // clusters of 1 to 8 CTAs that run at once on 148 SMs (a cluster lies in one GPC)
@@ -560,6 +561,12 @@ LinPlan plan_linear(int64_t M, int64_t N, int64_t K) {
     const int64_t tm = (M + f8::BM - 1) / f8::BM, blocks = (K + f8::BK - 1) / f8::BK;
     const int64_t wide = tm * ((N + 255) / 256), narrow = tm * ((N + 127) / 128);
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    if (M <= 2) {
+        // enough warps to keep the GPU's loads in flight, each with a chunk at least
+        int ks = 1;
+        while (ks < f8::few::WARPS && N * ks < 148 * 16 * f8::few::R && K > ks * f8::few::CHUNK) ks *= 2;
+        return {LinPlan::FEW, ks, 0, 0};
+    }
     LinPlan best{LinPlan::WIDE, 1, 0, 0};
     int64_t t_best = up(wide, 148) * (blocks + 5);
     if (narrow > 148) return best;
@@ -579,8 +586,20 @@ LinPlan plan_linear(int64_t M, int64_t N, int64_t K) {
 }
 
 template <typename T, bool SW_ROWS>
+evo_status_t launch_linear_few(const evo::fp8::LinParams& p, int ks, cudaStream_t stream) {
+    namespace few = evo::fp8::few;
+    const int64_t rows = (int64_t)few::R * (few::WARPS / ks);
+    const unsigned grid = (unsigned)((p.N + rows - 1) / rows);
+    if (p.M == 1) few::linear_kernel<T, SW_ROWS, 1><<<grid, 32 * few::WARPS, 0, stream>>>(p, ks);
+    else few::linear_kernel<T, SW_ROWS, 2><<<grid, 32 * few::WARPS, 0, stream>>>(p, ks);
+    g_launches += 1;
+    return cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
+}
+
+template <typename T, bool SW_ROWS>
 evo_status_t launch_linear(const evo::fp8::LinParams& p, const LinPlan& plan, void* workspace, cudaStream_t stream) {
     namespace f8 = evo::fp8;
+    if (plan.form == LinPlan::FEW) return launch_linear_few<T, SW_ROWS>(p, plan.S, stream);
     if (plan.form == LinPlan::WIDE) return launch_linear_as<T, SW_ROWS, f8::Wide>(p, 1, stream);
     if (plan.form == LinPlan::SPLIT) return launch_linear_as<T, SW_ROWS, f8::Split>(p, plan.S, stream);
     f8::LinParams parts = p;

@@ -274,7 +274,7 @@ __device__ __forceinline__ float row_sum(float v, int wpr, int warp, int first, 
 // takes blockDim / 32 / wpr * R rows at a time (R rows per warp, only with wpr == 1) and walks the
 // rows with the grid.  The weight stays in registers, and the next rows are loaded while these are
 // worked on: at 32 warps of one row an SM has 32 KB on its way, too little for HBM's latency
-// (196608 x 256 in bf16: 104 us, with the loads ahead TODO).
+// (196608 x 256 in bf16: 104 us, with the loads ahead 65).
 template <typename T, bool VEC, int NV, int R, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 && NV * R <= 2 ? 2 : 1) add_rms_norm_kernel(const NormParams p, const int wpr) {
     __shared__ float buf[2][32];

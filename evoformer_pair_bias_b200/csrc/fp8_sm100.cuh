@@ -98,7 +98,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 // The summing warps are what bounds the long sums: a block's 128 x BN results are read
 // from TMEM and added in the time the tensor core takes for the next (512 cycles at BN =
 // 256).  Sixteen warps of 64 columns each hide each other's waits; eight of 128 took 335
-// us on 8191 x 4096 x 8192 where sixteen take TODO (the MMAs and loads alone: 180).  They
+// us on 8191 x 4096 x 8192 where sixteen take 258 (the MMAs and loads alone: 180).  They
 // hold their sums and nothing that comes from global memory: scales and bias fetched into
 // their own registers spilled and waited for the load at the spill.
 
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else if (warp == 2) {
             // C scales of the rows from r0 on (the last row again past `rows`), block by block: 16
             // bytes a copy where the rows' scales lie side by side and aligned (12 single copies a
-            // block held 1024 x 131072 x 256 up: 69 us, 3 wide ones TODO), else one for each row.  The
+            // block held 1024 x 131072 x 256 up: 69 us, 3 wide ones 60), else one for each row.  The
             // control warps have 32 registers: a pointer for each copy would spill, and take the
             // summing warps' code along with it.
             auto side = [](const float* src, int64_t s_row, int64_t s_grp, int r0, int C, int rows) {
@@ -587,5 +587,134 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* part, int64
     }
 }
 
+// ------------------------------------------------------------- one or two rows of x
+// The same product for single tokens, bound by reading w once: no tensor core, whose tiles would
+// be nearly empty and whose blocks' results would be read one by one.  A warp takes R rows of w
+// and every KS-th chunk of 512 codes of them, a lane 16 codes of each (one scale block), as exact
+// products of halves added in fp32 (one instruction each on sm_100a); the lanes are added by
+// shuffles, the KS warps in order.  What counts is bytes on their way: four chunks of two rows in
+// each of 32 warps an SM read 1 x 8192 x 8192 in 18.6 us, two of four rows in 24 warps in 26.8
+// (and left a second wave), sixteen rows' worth of fp32 conversions in 28.8; the tiles took 22.7.
+namespace few {
+
+constexpr int R = 2, CHUNK = 512, WARPS = 8;
+
+struct Codes16 {
+    uint32_t w[4];
+    // codes k .. k + 15 of a row, zeros from K on; nothing behind the row's last code is read
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const uint8_t* row, int k, int K) {
+        if (WHOLE || k + 16 <= K) {
+            const uint4 a = *reinterpret_cast<const uint4*>(row + k);
+            w[0] = a.x;
+            w[1] = a.y;
+            w[2] = a.z;
+            w[3] = a.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 15; ++i)
+                if (k + i < K) w[i >> 2] |= (uint32_t)row[k + i] << (8 * (i & 3));
+        }
+    }
+    // as 16 halves, which hold every e4m3 value
+    __device__ __forceinline__ void halves(uint32_t* h) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[i]) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
+    }
+};
+// a + the product of two halves, one rounding.
+__device__ __forceinline__ float fma_half(uint16_t x, uint16_t y, float a) {
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(a) : "h"(x), "h"(y));
+    return a;
+}
+
+template <typename T, bool SW_ROWS, int M>
+__global__ void __launch_bounds__(32 * WARPS, M == 1 ? 4 : 2) linear_kernel(const LinParams p, const int ks) {
+    __shared__ float join[WARPS][R * M];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp / ks, part = warp - sub * ks;       // the block's sub-th R rows, this warp's chunks
+    const int64_t n0 = ((int64_t)blockIdx.x * (WARPS / ks) + sub) * R;
+    const uint8_t *x[M], *w[R];
+    const float *sx[M], *sw[R];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {                            // a row past the last one repeats it
+        const int r = min(m, p.M - 1);
+        x[m] = static_cast<const uint8_t*>(p.x) + r * p.ldx;
+        sx[m] = p.sx + r * p.sx_row;
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const int64_t n = min(n0 + j, (int64_t)p.N - 1);
+        w[j] = static_cast<const uint8_t*>(p.w) + n * p.ldw;
+        sw[j] = p.sw + (SW_ROWS ? n : n / 128) * p.sw_row;
+    }
+    float acc[R][M];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[j][m] = 0.f;
+    auto add = [&](int k, auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        Codes16 cw[R], cx[M];
+        float fw[R], f[M];
+        const int64_t b = k / BK;
+#pragma unroll
+        for (int j = 0; j < R; ++j) cw[j].template load<WHOLE>(w[j], k, p.K);
+#pragma unroll
+        for (int m = 0; m < M; ++m) cx[m].template load<WHOLE>(x[m], k, p.K);
+#pragma unroll
+        for (int j = 0; j < R; ++j) fw[j] = __ldg(sw[j] + b * p.sw_grp);
+#pragma unroll
+        for (int m = 0; m < M; ++m) f[m] = __ldg(sx[m] + b * p.sx_grp);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            uint32_t v[8];
+            cw[j].halves(v);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                uint32_t u[8];
+                cx[m].halves(u);                             // once for all j: the compiler keeps it
+                float a = 0.f, c = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    a = fma_half((uint16_t)v[i], (uint16_t)u[i], a);
+                    c = fma_half((uint16_t)(v[i] >> 16), (uint16_t)(u[i] >> 16), c);
+                }
+                acc[j][m] = fmaf(a + c, f[m] * fw[j], acc[j][m]);
+            }
+        }
+    };
+    if (n0 < p.N) {
+        const int last = p.K / CHUNK * CHUNK;                // whole chunks first, without a test a load
+        int k = part * CHUNK + 16 * lane;
+#pragma unroll (M == 1 ? 4 : 2)
+        for (; k < last; k += ks * CHUNK) add(k, std::true_type{});
+        if (k < p.K) add(k, std::false_type{});
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) acc[j][m] += __shfl_xor_sync(0xffffffffu, acc[j][m], o);
+            if (lane == 0) join[warp][j * M + m] = acc[j][m];
+        }
+    __syncthreads();
+    if (part == 0 && lane < R * M) {
+        float s = 0.f;
+        for (int i = 0; i < ks; ++i) s += join[warp + i][lane];
+        const int m = lane % M;
+        const int64_t n = n0 + lane / M;
+        if (m < p.M && n < p.N) {
+            if (p.bias) s += __ldg(p.bias + n);
+            Elem<T>::store(static_cast<T*>(p.y) + m * p.ldy + n, s);
+        }
+    }
+}
+
+}  // namespace few
 }  // namespace fp8
 }  // namespace evo

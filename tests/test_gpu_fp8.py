@@ -334,7 +334,8 @@ def check_linear(y, xq, xs, wq, ws, bias):
 SHAPES = [(1, 1, 1), (1, 128, 128), (3, 5, 17), (1, 4096, 4096), (128, 128, 128), (129, 127, 129), (64, 1024, 256),
           (200, 136, 4000), (5, 300, 12345), (257, 1000, 384), (300, 2048, 512), (1, 8, 8192), (17, 777, 1040),
           (2500, 1024, 256), (700, 1001, 130),
-          (1, 8192, 8192), (1, 3, 50000), (100, 77, 40001), (129, 257, 16384)]
+          (2, 77, 530), (3, 1000, 4097), (4, 129, 700), (4, 4096, 1024), (5, 4096, 1024), (2, 1, 8191),
+          (1, 8192, 8192), (1, 3, 50000), (6, 3, 50000), (100, 77, 40001), (129, 257, 16384)]
 
 
 @pytest.mark.parametrize("out_dtype", [BF16, F32])
@@ -569,7 +570,7 @@ def test_graph_replay_matches_eager():
 
 def test_calls_on_two_streams_do_not_disturb_each_other():
     g = gen(73)
-    sets = [operands(1, 4096, 4096, True, g) for _ in range(2)]
+    sets = [operands(8, 512, 16384, True, g) for _ in range(2)]   # both with a workspace
     want = [fp8.fp8_linear(*s) for s in sets]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
