@@ -37,7 +37,7 @@ EXPORTS = ("evo_attn_fwd", "evo_attn_bwd", "evo_attn_bwd_workspace_bytes", "evo_
            "evo_tri_mul", "evo_outer_product_mean", "evo_sum_partials", "evo_attn_set_wait_limit_ns",
            "evo_exp2_fma", "evo_add_rms_norm_fp8", "evo_add_rms_norm_bwd", "evo_add_rms_norm_bwd_workspace_bytes",
            "evo_quantize_fp8", "evo_quantize_fp8_both", "evo_fp8_linear",
-           "evo_fp8_linear_workspace_bytes")
+           "evo_fp8_linear_workspace_bytes", "evo_fp8_linear_bwd", "evo_fp8_linear_bwd_workspace_bytes")
 
 #: Default limit of the kernels' bounded waits (EVO_WAIT_LIMIT_NS), nanoseconds.
 DEFAULT_WAIT_LIMIT_NS = 2_000_000_000
@@ -136,6 +136,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.evo_fp8_linear.restype = ci
     lib.evo_fp8_linear_workspace_bytes.argtypes = [i64, i64, i64]
     lib.evo_fp8_linear_workspace_bytes.restype = ctypes.c_size_t
+    lib.evo_fp8_linear_bwd_workspace_bytes.argtypes = [i64, i64, i64, ci, ci]
+    lib.evo_fp8_linear_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.evo_fp8_linear_bwd.argtypes = [i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, vp, ci,
+                                       i64, vp, ctypes.c_size_t, vp]
+    lib.evo_fp8_linear_bwd.restype = ci
     _lib = lib
     return lib
 

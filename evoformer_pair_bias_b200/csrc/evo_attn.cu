@@ -393,11 +393,16 @@ RowSplit row_split_bwd(int64_t cols) {
     return {nv, wpr, 32 * (wpr <= 8 ? 8 / wpr * wpr : wpr)};
 }
 
-// Blocks for `rows` of which a block takes `per` at a time: at most what runs at once.
+// Blocks for `rows` of which a block takes `per` at a time: at most what runs at once.  The answer for
+// each block size is kept by the kernel's launcher (asking costs a microsecond).
+using Resident = std::atomic<int>[33];
 template <typename K>
-int walking_grid(K kernel, int threads, int64_t rows, int64_t per) {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+int walking_grid(K kernel, int threads, int64_t rows, int64_t per, Resident& kept) {
+    int n = kept[threads / 32].load();
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+        kept[threads / 32].store(n);
+    }
     return (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)sm_count() * n);
 }
 
@@ -411,7 +416,8 @@ void by_type(evo_dtype_t dtype, bool vec, F f) {
 template <typename T, bool VEC, int NV, int R, int THREADS>
 void launch_norm_as(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {
     auto kern = evo::fp8::add_rms_norm_kernel<T, VEC, NV, R, THREADS>;
-    const int grid = walking_grid(kern, s.threads, p.rows, s.threads / 32 / s.wpr * R);
+    static Resident kept;
+    const int grid = walking_grid(kern, s.threads, p.rows, s.threads / 32 / s.wpr * R, kept);
     kern<<<grid, s.threads, 0, stream>>>(p, s.wpr);
 }
 template <typename T, bool VEC>
@@ -1058,6 +1064,31 @@ evo_status_t evo_quantize_fp8_both(int64_t rows, int64_t cols, evo_dtype_t dtype
     return quantize(p, dtype, square != 0, static_cast<cudaStream_t>(stream));
 }
 
+// Where evo_fp8_linear_bwd keeps its operands in the workspace.
+struct BwdOperands {
+    int64_t ld_n, ld_m;          // pitches of dy's codes, and of both transposes
+    size_t dy, dys, dyt, dyts, xt, xts, work, total;
+    BwdOperands(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
+        const int64_t gn = (N + 127) / 128, gm = (M + 127) / 128;
+        ld_n = (N + 15) / 16 * 16;
+        ld_m = (M + 15) / 16 * 16;
+        size_t at = 0;
+        auto take = [&](bool want, int64_t bytes) {
+            const size_t here = at;
+            if (want) at += align256((size_t)bytes);
+            return here;
+        };
+        dy = take(dx, M * ld_n);
+        dys = take(dx, M * gn * 4);
+        dyt = take(dw, N * ld_m);
+        dyts = take(dw, N * gm * 4);
+        xt = take(dw, K * ld_m);
+        xts = take(dw, K * gm * 4);
+        work = at;
+        total = at + std::max(dx ? plan_linear(M, K, N).workspace : 0, dw ? plan_linear(N, K, M).workspace : 0);
+    }
+};
+
 size_t evo_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     const int64_t most = (int64_t)0x7fffffff - 256;
     return M < 1 || N < 1 || K < 1 || M > most || N > most || K > most ? 0 : plan_linear(M, N, K).workspace;
@@ -1092,6 +1123,62 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
     if (y_dtype == EVO_DTYPE_BF16)
         return w_scale_rows ? launch_linear<__nv_bfloat16, true>(p, plan, workspace, s) : launch_linear<__nv_bfloat16, false>(p, plan, workspace, s);
     return w_scale_rows ? launch_linear<float, true>(p, plan, workspace, s) : launch_linear<float, false>(p, plan, workspace, s);
+}
+
+size_t evo_fp8_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int want_dx, int want_dw) {
+    const int64_t most = (int64_t)0x7fffffff - 256;
+    if (M < 1 || N < 1 || K < 1 || M > most || N > most || K > most) return 0;
+    return BwdOperands(M, N, K, want_dx != 0, want_dw != 0).total;
+}
+
+evo_status_t evo_fp8_linear_bwd(int64_t M, int64_t N, int64_t K, evo_dtype_t dtype, const void* dy, int64_t lddy,
+                                const void* x, int64_t ldx, const void* w_t, int64_t ldw_t, const float* w_t_scale,
+                                int64_t w_t_scale_row, int64_t w_t_scale_group, void* dx, int64_t lddx, void* dw,
+                                evo_dtype_t dw_dtype, int64_t lddw, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (M < 0 || N < 0 || K < 1 || !dtype_ok(dtype) || !dtype_ok(dw_dtype)) return EVO_ERR_INVALID_ARG;
+    if (N == 0 || (!dx && !dw)) return EVO_OK;
+    if (dw && N > 1 && lddw < K) return EVO_ERR_INVALID_ARG;
+    if (M == 0) {                                           // the empty sum
+        const size_t e = (size_t)elem_bytes(dw_dtype);
+        if (dw && cudaMemset2DAsync(dw, (size_t)(N > 1 ? lddw : K) * e, 0, (size_t)K * e, (size_t)N,
+                                    static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return EVO_ERR_CUDA;
+        return EVO_OK;
+    }
+    const int64_t most = (int64_t)0x7fffffff - 256;
+    if (M > most || N > most || K > most) return EVO_ERR_UNSUPPORTED;
+    if (!dy || (dw && !x) || (dx && (!w_t || !w_t_scale)) || (dx && M > 1 && lddx < K)) return EVO_ERR_INVALID_ARG;
+    if ((dx && !aligned(dx, elem_bytes(dtype))) || (dw && !aligned(dw, elem_bytes(dw_dtype)))) return EVO_ERR_INVALID_ARG;
+    // everything the calls below would refuse, before the first of them enqueues anything
+    if (lddy < 0 || !aligned(dy, elem_bytes(dtype)) || (dw && (ldx < 0 || !aligned(x, elem_bytes(dtype)))))
+        return EVO_ERR_INVALID_ARG;
+    if (dx && ((K > 1 && ldw_t < N) || w_t_scale_row < 0 || w_t_scale_group < 0 || !aligned(w_t_scale, 4)))
+        return EVO_ERR_INVALID_ARG;
+    if (dx && (!aligned(w_t, 16) || (K > 1 && ldw_t % 16 != 0))) return EVO_ERR_UNSUPPORTED;
+    const BwdOperands o(M, N, K, dx != nullptr, dw != nullptr);
+    if (!workspace || workspace_bytes < o.total) return EVO_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 256)) return EVO_ERR_INVALID_ARG;
+    char* ws = static_cast<char*>(workspace);
+    auto f = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    const size_t work = workspace_bytes - o.work;
+    evo_status_t st;
+    if (dx && dw)
+        st = evo_quantize_fp8_both(M, N, dtype, dy, lddy, 0, ws + o.dy, o.ld_n, f(o.dys), 1, M, ws + o.dyt, o.ld_m,
+                                   f(o.dyts), 1, N, stream);
+    else if (dx)
+        st = evo_quantize_fp8(M, N, dtype, dy, lddy, 0, 0, ws + o.dy, o.ld_n, f(o.dys), 1, M, stream);
+    else
+        st = evo_quantize_fp8(M, N, dtype, dy, lddy, 0, 1, ws + o.dyt, o.ld_m, f(o.dyts), 1, N, stream);
+    if (st == EVO_OK && dx)
+        st = evo_fp8_linear(M, K, N, ws + o.dy, o.ld_n, f(o.dys), 1, M, w_t, ldw_t, w_t_scale, w_t_scale_row,
+                            w_t_scale_group, 0, nullptr, dtype, dx, lddx, ws + o.work, work, stream);
+    if (st == EVO_OK && dw)
+        st = evo_quantize_fp8(M, K, dtype, x, ldx, 0, 1, ws + o.xt, o.ld_m, f(o.xts), 1, K, stream);
+    if (st == EVO_OK && dw)
+        st = evo_fp8_linear(N, K, M, ws + o.dyt, o.ld_m, f(o.dyts), 1, N, ws + o.xt, o.ld_m, f(o.xts), 1, K, 1, nullptr,
+                            dw_dtype, dw, lddw, ws + o.work, work, stream);
+    return st;
 }
 
 }  // extern "C"

@@ -71,6 +71,12 @@ __device__ __forceinline__ uint64_t quotient(uint64_t v, const Divisor& d) {
     const uint64_t t = fmul2(v, twice(0.875f)), q = fmul2(t, d.inv);
     return ffma2(ffma2(q, d.neg, t), d.inv, q);
 }
+// The same of v + low, the rounding of 0.875 v included: what fp32 values have that bf16 ones do not.
+__device__ __forceinline__ uint64_t quotient(uint64_t v, uint64_t low, const Divisor& d) {
+    const uint64_t c = twice(0.875f), t = fmul2(v, c), q = fmul2(t, d.inv);
+    const uint64_t left = ffma2(c, low, ffma2(c, v, t ^ 0x8000000080000000ull));
+    return ffma2(fadd2(ffma2(q, d.neg, t), left), d.inv, q);
+}
 // Four quotients as e4m3 bytes.
 __device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b, const Divisor& d) {
     return e4m3x2(quotient(a, d)) | (e4m3x2(quotient(b, d)) << 16);
@@ -185,17 +191,22 @@ __device__ __forceinline__ void group_max(const uint64_t* v, uint32_t* mag) {
 }
 
 // The fragment's quotients, m[0] / m[1] the divisors of its two halves, as bytes of q's row.
-// q rows are 16-byte aligned; only columns below `cols` are written.
+// q rows are 16-byte aligned; only columns below `cols` are written.  `low`: what is left of each
+// value beyond fp32, or null.
 template <bool VEC>
 __device__ __forceinline__ void store_e4m3(uint8_t* row, int64_t c0, int64_t cols, int lane, const uint64_t* v,
-                                           const float* m) {
+                                           const float* m, const uint64_t* low = nullptr) {
+    auto four = [&](int i, const Divisor& d) {
+        if (!low) return e4m3x4(v[i], v[i + 1], d);
+        return e4m3x2(quotient(v[i], low[i], d)) | (e4m3x2(quotient(v[i + 1], low[i + 1], d)) << 16);
+    };
     const Divisor d0(m[0]);
-    const uint32_t lo = e4m3x4(v[0], v[1], d0);
+    const uint32_t lo = four(0, d0);
     uint32_t hi;
     if (VEC)
-        hi = e4m3x4(v[2], v[3], d0);
+        hi = four(2, d0);
     else
-        hi = e4m3x4(v[2], v[3], Divisor(m[1]));
+        hi = four(2, Divisor(m[1]));
     if (VEC) {
         const int64_t c = c0 + 8 * lane;
         if (c + 8 <= cols)
@@ -349,7 +360,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && NV * R <= 2 ? 2 : 1
                     m[g] = divisor(mag[g], least[k]);
                     sc[g] = m[g] * per_m[k];
                 }
-                store_e4m3<VEC>(p.q + row * p.ldq, c0, p.cols, lane, u, m);
+                if constexpr (sizeof(T) == 4) {            // fp32: u is rounded, its rest goes into the quotient
+                    uint64_t low[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) low[e] = ffma2(h[k][i].pair(e), w[i][e], u[e] ^ 0x8000000080000000ull);
+                    store_e4m3<VEC>(p.q + row * p.ldq, c0, p.cols, lane, u, m, low);
+                } else {
+                    store_e4m3<VEC>(p.q + row * p.ldq, c0, p.cols, lane, u, m);
+                }
                 store_scales<VEC>(p.scale + row * p.s_row, p.s_grp, c0, p.cols, lane, sc);
             }
         }

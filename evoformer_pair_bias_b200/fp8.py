@@ -309,23 +309,46 @@ def _forward(ctx, q, scale, w, dtype):
     return fp8_linear(q, scale, wq, ws, out_dtype=dtype), wqt, wst
 
 
-def _gradients(dy, wqt, wst, x, w_dtype, want_dx, want_dw):
-    """(dy @ w, dy^T @ x) in 8 bits: groups of 128 outputs, and of 128 rows."""
-    dx = dw = None
-    if want_dw and dy.numel() == 0:              # the empty sum
-        dw = torch.zeros((dy.shape[-1], x.shape[-1]), dtype=w_dtype, device=dy.device)
-        want_dw = False
-    if want_dx and want_dw:
-        q, s, qt, st = quantize_fp8_both(dy)
-    elif want_dx:
-        q, s = quantize_fp8(dy)
-    elif want_dw:
-        qt, st = quantize_fp8(dy, transpose=True)
-    if want_dx:
-        dx = fp8_linear(q, s, wqt, wst, out_dtype=dy.dtype)
+def fp8_linear_bwd(dy, x, wq_t, w_scale_t, dw_dtype=torch.float32, want_dx=True, want_dw=True):
+    """Gradients of ``y = x @ w.T`` in 8 bits: ``(dx, dw)``, each None where it is not wanted.
+
+    dy ``[..., N]`` and x ``[..., K]`` (bf16 or fp32, one type) are quantised here; wq_t ``[K, N]`` and
+    w_scale_t are the transposed half of ``quantize_fp8_both(w, square=True)``.  dx ``[..., K]`` is of
+    dy's type, dw ``[N, K]`` of dw_dtype.  x may be None without dw, wq_t and w_scale_t without dx.
+    """
+    dev = _on(dy, x, wq_t, w_scale_t)
+    dtype, shape = dy.dtype, dy.shape
+    dt = _dtype(dy, "dy")
+    if dw_dtype not in DTYPES:
+        raise ValueError(f"dw_dtype must be bf16 or fp32, got {dw_dtype}")
+    M, N, dy2, lddy = _rows(dy)
+    dx = dw = x2 = None
+    ldx = w_at = ldw = s_at = sr = sg = nbytes = 0
     if want_dw:
-        dw = fp8_linear(qt, st, *quantize_fp8(x, transpose=True), out_dtype=w_dtype)
-    return dx, dw
+        if x is None or x.dtype != dtype or x.shape[:-1] != shape[:-1]:
+            raise ValueError("x must have dy's type and leading axes")
+        x2, ldx = _rows(x)[2:]
+        K = x.shape[-1]
+        dw = _empty((N, K), (K, 1), dtype=dw_dtype, device=dev)
+    if want_dx:
+        wk, wn, w_at, ldw = _codes(wq_t, "wq_t")
+        if wn != N or (want_dw and wk != K):
+            raise ValueError(f"wq_t must be [K, {N}], got {tuple(wq_t.shape)}")
+        K = wk
+        if w_scale_t.shape != (-(-K // GROUP), -(-N // GROUP)) or w_scale_t.dtype != torch.float32:
+            raise ValueError(f"w_scale_t must be fp32 of shape {(-(-K // GROUP), -(-N // GROUP))}")
+        sr, sg = w_scale_t.stride()
+        s_at = w_scale_t.data_ptr()
+        dx = _empty((M, K), (K, 1), dtype=dtype, device=dev)
+    if dx is None and dw is None:
+        return None, None
+    ws = None
+    nbytes = load_library().evo_fp8_linear_bwd_workspace_bytes(M, N, K, want_dx, want_dw)
+    if nbytes:
+        ws = _empty((nbytes,), (1,), dtype=torch.uint8, device=dev)
+    _call("evo_fp8_linear_bwd", dev, M, N, K, dt, dy2.data_ptr(), lddy, _addr(x2), ldx, w_at, ldw, s_at, sr, sg,
+          _addr(dx), K, _addr(dw), DTYPES[dw_dtype], K, _addr(ws), nbytes)
+    return dx if dx is None or len(shape) == 2 else dx.view(*shape[:-1], K), dw
 
 
 class Fp8Linear(torch.autograd.Function):
@@ -342,7 +365,7 @@ class Fp8Linear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, wqt, wst = ctx.saved_tensors
-        return _gradients(dy, wqt, wst, x, ctx.w_dtype, *ctx.needs_input_grad)
+        return fp8_linear_bwd(dy, x, wqt, wst, ctx.w_dtype, *ctx.needs_input_grad)
 
 
 class AddRmsNormLinear(torch.autograd.Function):
@@ -366,7 +389,7 @@ class AddRmsNormLinear(torch.autograd.Function):
         for_x, for_res, for_weight, _, for_w = ctx.needs_input_grad
         if dy is None:
             return dh if for_x else None, dh if for_res else None, None, None, None
-        dn, dw = _gradients(dy, wqt, wst, n, ctx.w_dtype, for_x or for_res or for_weight, for_w)
+        dn, dw = fp8_linear_bwd(dy, n, wqt, wst, ctx.w_dtype, for_x or for_res or for_weight, for_w)
         dx = dweight = None
         if dn is not None:
             dx, dweight = add_rms_norm_bwd(dn, dh, h, rstd, weight, for_weight,

@@ -301,7 +301,7 @@ evo_status_t evo_outer_product_mean(int64_t B, int64_t S, int64_t N, int64_t Ca,
 evo_status_t evo_sum_partials(int64_t count, const float* const* parts, int64_t n, float* out, void* stream);
 
 /*
- * The 8-bit projection.  The four calls below take the rows of a residual
+ * The 8-bit projection.  The calls below take the rows of a residual
  * stream through a projection in 8-bit floating point and back: the norm in
  * front of it, the quantiser for weights, other activations and gradients,
  * the product, and the norm's gradient.  The product's output is bf16 or
@@ -425,6 +425,28 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
                             const float* w_scale, int64_t w_scale_row, int64_t w_scale_group, int w_scale_rows,
                             const float* bias, evo_dtype_t y_dtype, void* y, int64_t ldy, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of y = x @ w^T computed in 8 bits, with the rounding to 8 bits
+ * passed over: dy [M, N] and x [M, K] of `dtype` (row pitches lddy, ldx) are
+ * quantised here -- dy in 1 x 128 groups along N, and along M together with x
+ * -- and w comes transposed, w_t [K, N] with its 128 x 128 block scales, as
+ * evo_quantize_fp8_both left it in the forward:
+ *
+ *   dx [M, K] = Q(dy) @ Q(w)             of dtype; NULL: not computed
+ *   dw [N, K] = Q(dy^T) @ Q(x^T)^T       of dw_dtype; NULL: not computed
+ *
+ * x may be NULL without dw, w_t and its scales without dx.  workspace: at
+ * least evo_fp8_linear_bwd_workspace_bytes(M, N, K, dx, dw) bytes, 256-byte
+ * aligned, contents arbitrary; calls that may overlap need one each.  M == 0
+ * sets dw to zero.
+ */
+size_t evo_fp8_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int want_dx, int want_dw);
+evo_status_t evo_fp8_linear_bwd(int64_t M, int64_t N, int64_t K, evo_dtype_t dtype, const void* dy, int64_t lddy,
+                                const void* x, int64_t ldx, const void* w_t, int64_t ldw_t, const float* w_t_scale,
+                                int64_t w_t_scale_row, int64_t w_t_scale_group, void* dx, int64_t lddx, void* dw,
+                                evo_dtype_t dw_dtype, int64_t lddw, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* evo_status_string(evo_status_t status);

@@ -120,6 +120,23 @@ def test_linear_refusals(lib):
         assert need(M, N, K) <= 148 * 128 * 256 * 4 + (1 << 22)                   # bounded by the GPU, not by K
 
 
+def test_linear_bwd_refusals_and_workspace(lib):
+    need = lib.evo_fp8_linear_bwd_workspace_bytes
+    assert need(0, 8, 8, 1, 1) == 0 and need(8, 0, 8, 1, 1) == 0 and need(8, 8, 0, 1, 1) == 0
+    assert need(300, 64, 128, 1, 0) < need(300, 64, 128, 1, 1) and need(300, 64, 128, 0, 1) < need(300, 64, 128, 1, 1)
+
+    def f(M=8, N=8, K=64, dt=0, dy=FAKE, lddy=8, x=FAKE, ldx=64, w=FAKE, ldw=16, ws=FAKE, wr=1, dx=FAKE, lddx=64, dw=FAKE,
+          dwd=1, lddw=64, work=FAKE, nb=1 << 30):
+        return lib.evo_fp8_linear_bwd(M, N, K, dt, dy, lddy, x, ldx, w, ldw, ws, wr, 1, dx, lddx, dw, dwd, lddw, work, nb,
+                                      NUL)
+    assert f(N=0, dy=NUL) == 0 and f(dx=NUL, dw=NUL, dy=NUL) == 0 and f(M=0, dw=NUL, dy=NUL) == 0
+    assert f(M=-1) == 1 and f(K=0) == 1 and f(dt=3) == 1 and f(dwd=3) == 1 and f(lddw=8) == 1 and f(lddx=8) == 1
+    assert f(dy=NUL) == 1 and f(x=NUL) == 1 and f(w=NUL) == 1 and f(ws=NUL) == 1 and f(wr=-1) == 1 and f(ldx=-1) == 1
+    assert f(dt=1, dx=ODD) == 1 and f(dw=ODD) == 1 and f(dt=1, dy=ODD) == 1 and f(dt=1, x=ODD) == 1
+    assert f(ldw=24) == 2 and f(w=ODD4) == 2 and f(M=1 << 31) == 2
+    assert f(nb=100) == 3 and f(work=NUL) == 3 and f(work=ODD4) == 1
+
+
 def test_binding_refusals():
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
