@@ -547,6 +547,9 @@ evo_status_t launch_linear_as(const evo::fp8::LinParams& p, int S, cudaStream_t 
     return err == cudaSuccess && cudaGetLastError() == cudaSuccess ? EVO_OK : EVO_ERR_CUDA;
 }
 
+// Largest size of a product's axis: every index and step of the kernels stays below 2^31.
+constexpr int64_t kMaxProduct = (int64_t)0x7fffffff - 65536;
+
 // Which form a product takes: Few with S warps a row of w, Wide (S = 1), Split with S CTAs a tile, or
 // Parts with S runs a tile.
 struct LinPlan {
@@ -1090,8 +1093,7 @@ struct BwdOperands {
 };
 
 size_t evo_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    const int64_t most = (int64_t)0x7fffffff - 256;
-    return M < 1 || N < 1 || K < 1 || M > most || N > most || K > most ? 0 : plan_linear(M, N, K).workspace;
+    return M < 1 || N < 1 || K < 1 || M > kMaxProduct || N > kMaxProduct || K > kMaxProduct ? 0 : plan_linear(M, N, K).workspace;
 }
 
 evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const float* x_scale,
@@ -1108,8 +1110,7 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
         return EVO_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(w, 16) || (M > 1 && ldx % 16 != 0) || (N > 1 && ldw % 16 != 0))
         return EVO_ERR_UNSUPPORTED;
-    const int64_t most = (int64_t)0x7fffffff - 256;
-    if (M > most || N > most || K > most) return EVO_ERR_UNSUPPORTED;
+    if (M > kMaxProduct || N > kMaxProduct || K > kMaxProduct) return EVO_ERR_UNSUPPORTED;
     const LinPlan plan = plan_linear(M, N, K);
     if (plan.workspace > 0 && (!workspace || workspace_bytes < plan.workspace)) return EVO_ERR_WORKSPACE_TOO_SMALL;
     if (plan.workspace > 0 && !aligned(workspace, 256)) return EVO_ERR_INVALID_ARG;
@@ -1126,8 +1127,7 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
 }
 
 size_t evo_fp8_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int want_dx, int want_dw) {
-    const int64_t most = (int64_t)0x7fffffff - 256;
-    if (M < 1 || N < 1 || K < 1 || M > most || N > most || K > most) return 0;
+    if (M < 1 || N < 1 || K < 1 || M > kMaxProduct || N > kMaxProduct || K > kMaxProduct) return 0;
     return BwdOperands(M, N, K, want_dx != 0, want_dw != 0).total;
 }
 
@@ -1146,8 +1146,7 @@ evo_status_t evo_fp8_linear_bwd(int64_t M, int64_t N, int64_t K, evo_dtype_t dty
             return EVO_ERR_CUDA;
         return EVO_OK;
     }
-    const int64_t most = (int64_t)0x7fffffff - 256;
-    if (M > most || N > most || K > most) return EVO_ERR_UNSUPPORTED;
+    if (M > kMaxProduct || N > kMaxProduct || K > kMaxProduct) return EVO_ERR_UNSUPPORTED;
     if (!dy || (dw && !x) || (dx && (!w_t || !w_t_scale)) || (dx && M > 1 && lddx < K)) return EVO_ERR_INVALID_ARG;
     if ((dx && !aligned(dx, elem_bytes(dtype))) || (dw && !aligned(dw, elem_bytes(dw_dtype)))) return EVO_ERR_INVALID_ARG;
     // everything the calls below would refuse, before the first of them enqueues anything

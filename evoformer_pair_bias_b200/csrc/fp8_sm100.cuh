@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!L::JOIN && lane == 0) bulk_wait<0>();
     }
+    __syncwarp();                                          // one lane of the first warps comes late
     if constexpr (L::JOIN) {
         const int m0 = t0 / tn * BM, n0 = t0 % tn * BN;
         cluster_sync();

@@ -21,6 +21,7 @@ over by the gradient.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .attention import DTYPES, EVO_OK, EvoError, _opt_f32, load_library
 
@@ -363,6 +364,7 @@ class Fp8Linear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, wqt, wst = ctx.saved_tensors
         return fp8_linear_bwd(dy, x, wqt, wst, ctx.w_dtype, *ctx.needs_input_grad)
@@ -384,6 +386,7 @@ class AddRmsNormLinear(torch.autograd.Function):
         return h, y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, dy):
         h, rstd, n, weight, wqt, wst = ctx.saved_tensors
         for_x, for_res, for_weight, _, for_w = ctx.needs_input_grad

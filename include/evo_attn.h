@@ -415,7 +415,8 @@ evo_status_t evo_quantize_fp8_both(int64_t rows, int64_t cols, evo_dtype_t dtype
  * the sizes: the same bits on every run.  workspace: device buffer of at least
  * evo_fp8_linear_workspace_bytes(M, N, K) bytes (0 for most sizes: then it may
  * be NULL), 256-byte aligned, contents arbitrary; calls that may overlap need
- * one each.  K >= 1; M == 0 or N == 0 is a no-op.  Waits in the
+ * one each.  K >= 1; M == 0 or N == 0 is a no-op; sizes up to 2^31 - 65537
+ * (EVO_ERR_UNSUPPORTED above).  Waits in the
  * kernel are bounded, and one that gives up is reported by
  * evo_attn_device_status.
  */

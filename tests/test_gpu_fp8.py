@@ -195,7 +195,8 @@ def check_norm(x, res, w, eps, out, want_n=False):
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (3, 7), (17, 64), (9, 128), (1000, 256), (129, 257),
                                        (40, 512), (33, 1000), (65, 1024), (20, 2500), (7, 5001), (4, 8192),
-                                       (3, 9000), (2, 16384), (2, 32768), (3, 32767)])
+                                       (3, 9000), (2, 16384), (2, 32768), (3, 32767), (700, 700), (301, 1500), (50, 2049),
+                                       (9, 4100), (4, 10300)])
 def test_add_rms_norm(rows, cols, residual, dtype, wdtype):
     g = gen(rows * 7 + cols)
     x = stream_rows(rows, cols, g, dtype)
@@ -262,7 +263,8 @@ def test_add_rms_norm_in_place_on_the_residual_stream():
 @pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, None)])
 @pytest.mark.parametrize("stream", [True, False])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (3, 7), (17, 64), (1000, 256), (129, 257), (40, 512),
-                                       (33, 1000), (6001, 1024), (20, 2500), (7, 5001), (3, 9000), (2, 32767)])
+                                       (33, 1000), (6001, 1024), (20, 2500), (7, 5001), (3, 9000), (2, 32767), (700, 700), (301, 1500), (50, 2049),
+                                       (400, 4100), (4, 10300)])
 def test_add_rms_norm_bwd(rows, cols, stream, dtype, wdtype):
     g = gen(rows * 13 + cols)
     h = stream_rows(rows, cols, g, dtype)
@@ -398,6 +400,30 @@ def test_fp8_linear_nan_scales_reach_their_rows_only():
     bad = torch.zeros(300, dtype=torch.bool, device="cuda")
     bad[[7, 299]] = True
     assert y[bad].isnan().all() and torch.isfinite(y[~bad]).all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 70, 20000])
+def test_fp8_linear_nan_codes(M):
+    # a NaN code under a finite scale: its row of y, and in w its column
+    g = gen(44)
+    xq, xs = fp8.quantize_fp8(randn((M, 300), g, BF16))
+    wq, ws = fp8.quantize_fp8(randn((140, 300), g, BF16), square=True)
+    xq.view(torch.uint8)[M - 1, 299] = 0x7F
+    wq.view(torch.uint8)[5, 7] = 0xFF
+    y = fp8.fp8_linear(xq, xs, wq, ws)
+    bad = torch.zeros((M, 140), dtype=torch.bool, device="cuda")
+    bad[M - 1] = True
+    bad[:, 5] = True
+    assert torch.equal(y.isnan(), bad)
+
+
+def test_training_functions_are_once_differentiable():
+    g = gen(45)
+    x, w = randn((8, 64), g, BF16).requires_grad_(True), randn((16, 64), g, BF16).requires_grad_(True)
+    dy = randn((8, 16), g, BF16).requires_grad_(True)
+    (gx,) = torch.autograd.grad(fp8.fp8_linear_train(x, w), x, dy, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        gx.sum().backward()
 
 
 def test_fp8_linear_leading_axes_and_empty_calls():
