@@ -97,11 +97,11 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 //
 // The summing warps are what bounds the long sums: a block's 128 x BN results are read
 // from TMEM and added in the time the tensor core takes for the next (512 cycles at BN =
-// 256).  Sixteen warps of 64 columns each hide each other's waits; eight of 128 took 335
-// us on 8191 x 4096 x 8192 where sixteen take 258 (the MMAs and loads alone: 180).  They
-// hold their sums and nothing that comes from global memory: scales and bias fetched into
-// their own registers spilled and waited for the load at the spill.
-
+// 256).  Sixteen warps of 64 columns hide each other's waits and share a tile's way out:
+// 131072 x 256 x 1024 takes 63 us, 8191 x 4096 x 8192 takes 260 (the MMAs and loads alone:
+// 180); eight of 128 columns need fewer instructions and take 71 and 250.  They hold their
+// sums and nothing that comes from global memory: scales and bias fetched into their own
+// registers spilled and waited for the load at the spill (125 us and 350).
 constexpr int SUM_WARPS = 16;                              // 4 column groups x 4 lane quarters
 constexpr int THREADS = 32 * (4 + SUM_WARPS);
 constexpr int RING = 8;                                    // blocks whose scales are held
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* part, int64
 // products of halves added in fp32 (one instruction each on sm_100a); the lanes are added by
 // shuffles, the KS warps in order.  What counts is bytes on their way: four chunks of two rows in
 // each of 32 warps an SM read 1 x 8192 x 8192 in 18.6 us, two of four rows in 24 warps in 26.8
-// (and left a second wave), sixteen rows' worth of fp32 conversions in 28.8; the tiles took 22.7.
+// (and left a second wave), with the codes converted to fp32 in 28.8; the tiles took 22.7.
 namespace few {
 
 constexpr int R = 2, CHUNK = 512, WARPS = 8;
