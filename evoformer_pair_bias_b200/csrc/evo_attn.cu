@@ -378,18 +378,18 @@ struct RowSplit {
     int nv, wpr, threads;
 };
 constexpr int64_t kMaxRowCols = 32768;
-// Forward: blocks of up to 8 warps, as many rows in them as fit; more fragments per warp for wider
-// rows.  Above 8192 columns up to 32 warps of four.
+// Forward: as many rows as fit in blocks of 8 warps, two fragments per warp above 2048 columns, up to
+// 16 warps (4097 columns in fp32: four fragments in five warps took 251 us where this takes TODO).
+// Above 8192 columns up to 32 warps of four.
 RowSplit row_split(int64_t cols) {
     const int chunks = (int)((cols + 255) / 256);
-    const int nv = chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4, wpr = (chunks + nv - 1) / nv;
+    const int nv = chunks <= 8 ? 1 : chunks <= 32 ? 2 : 4, wpr = (chunks + nv - 1) / nv;
     return {nv, wpr, 32 * (wpr <= 8 ? 8 / wpr * wpr : wpr)};
 }
-// Backward: twice the values per column, so one fragment per warp up to 20 warps (102 registers
-// each), two up to 40 chunks.
+// Backward: twice the values per column, so one fragment per warp up to 8192 columns.
 RowSplit row_split_bwd(int64_t cols) {
     const int chunks = (int)((cols + 255) / 256);
-    const int nv = chunks <= 20 ? 1 : chunks <= 40 ? 2 : 4, wpr = (chunks + nv - 1) / nv;
+    const int nv = chunks <= 32 ? 1 : 4, wpr = (chunks + nv - 1) / nv;
     return {nv, wpr, 32 * (wpr <= 8 ? 8 / wpr * wpr : wpr)};
 }
 
@@ -423,11 +423,11 @@ void launch_norm_as(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream
 template <typename T, bool VEC>
 void launch_norm(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {
     constexpr int R = sizeof(T) == 2 ? 2 : 1;    // fp32 rows fill the registers one at a time
-    if (s.threads > 256) return launch_norm_as<T, VEC, 4, 1, 1024>(p, s, stream);
+    if (s.nv == 4) return launch_norm_as<T, VEC, 4, 1, 1024>(p, s, stream);
+    if (s.threads > 256) return launch_norm_as<T, VEC, 2, 1, 512>(p, s, stream);
     if (s.wpr == 1) return launch_norm_as<T, VEC, 1, R, 256>(p, s, stream);
     if (s.nv == 1) return launch_norm_as<T, VEC, 1, 1, 256>(p, s, stream);
-    if (s.nv == 2) return launch_norm_as<T, VEC, 2, 1, 256>(p, s, stream);
-    return launch_norm_as<T, VEC, 4, 1, 256>(p, s, stream);
+    return launch_norm_as<T, VEC, 2, 1, 256>(p, s, stream);
 }
 
 template <typename T, bool VEC, int NV, int R, int THREADS>
@@ -439,8 +439,8 @@ void launch_norm_bwd_as(const evo::fp8::NormBwdParams& p, const RowSplit& s, int
 template <typename T, bool VEC>
 void launch_norm_bwd(const evo::fp8::NormBwdParams& p, const RowSplit& s, int grid, cudaStream_t stream) {
     constexpr int R = sizeof(T) == 2 ? 2 : 1;
-    if (s.threads > 640 || s.nv == 4) return launch_norm_bwd_as<T, VEC, 4, 1, 1024>(p, s, grid, stream);
-    if (s.nv == 2) return launch_norm_bwd_as<T, VEC, 2, 1, 640>(p, s, grid, stream);
+    if (s.nv == 4) return launch_norm_bwd_as<T, VEC, 4, 1, 1024>(p, s, grid, stream);
+    if (s.threads > 640) return launch_norm_bwd_as<T, VEC, 1, 1, 1024>(p, s, grid, stream);
     if (s.wpr == 1) return launch_norm_bwd_as<T, VEC, 1, R, 256>(p, s, grid, stream);
     return launch_norm_bwd_as<T, VEC, 1, 1, 640>(p, s, grid, stream);
 }

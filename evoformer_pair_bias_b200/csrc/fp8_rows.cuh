@@ -92,19 +92,78 @@ __device__ __forceinline__ float divisor(uint32_t mag, float least = LEAST) {
 
 // ------------------------------------------------------------- row fragments
 // A warp holds 256 columns of a row, 8 values a lane.
-//   VEC   lane l holds columns 8l .. 8l + 7 (16-byte loads): a 128-group is a half warp
+//   run   lane l holds columns 8l .. 8l + 7: a 128-group is a half warp.  bf16, and fp32 where VEC
 //   else  lane l holds columns l + 32e (single loads, coalesced): values 0..3 lie in
 //         the first group, 4..7 in the second
-// VEC wants every row 16-byte aligned and the row's bytes a multiple of 16.
+// VEC: every row is 16-byte aligned and the row's bytes are a multiple of 16, so a run is read
+// 16 bytes at a time.  Other bf16 rows are read by aligned words, with a single value at either
+// end of a run that starts at an odd one.
 // Raw is a fragment as loaded, so that the next one can be on its way meanwhile.
-template <bool VEC>
+template <typename T, bool VEC>
+constexpr bool kRun = VEC || sizeof(T) == 2;
+template <bool RUN>
 __device__ __forceinline__ int frag_col(int lane, int e) {
-    return VEC ? 8 * lane + e : lane + 32 * e;
+    return RUN ? 8 * lane + e : lane + 32 * e;
+}
+
+// Eight bf16 values from p, of which the first `n` exist, as four pairs; zeros for the others.
+__device__ __forceinline__ void load_run(const __nv_bfloat16* p, int64_t n, uint32_t* w) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    if (n >= 8) {
+        if ((reinterpret_cast<uintptr_t>(h) & 2) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(h + 2 * i);
+        } else {
+            const uint32_t first = h[0], last = h[7];
+            uint32_t m[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) m[i] = *reinterpret_cast<const uint32_t*>(h + 1 + 2 * i);
+            w[0] = first | (m[0] << 16);
+            w[1] = __funnelshift_r(m[0], m[1], 16);
+            w[2] = __funnelshift_r(m[1], m[2], 16);
+            w[3] = (m[2] >> 16) | (last << 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = 0;
+            if (2 * i < n) w[i] = h[2 * i];
+            if (2 * i + 1 < n) w[i] |= (uint32_t)h[2 * i + 1] << 16;
+        }
+    }
+}
+__device__ __forceinline__ void store_run(__nv_bfloat16* p, int64_t n, const uint32_t* w) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(p);
+    if (n >= 8) {
+        if ((reinterpret_cast<uintptr_t>(h) & 2) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(h + 2 * i) = w[i];
+        } else {
+            h[0] = (uint16_t)w[0];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(h + 1 + 2 * i) = __funnelshift_r(w[i], w[i + 1], 16);
+            h[7] = (uint16_t)(w[3] >> 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) h[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+}
+// Eight codes to q's row at column c (a multiple of 8; rows are 16-byte aligned), below `cols` only.
+__device__ __forceinline__ void store_codes(uint8_t* row, int64_t c, int64_t cols, uint32_t lo, uint32_t hi) {
+    if (c + 8 <= cols) {
+        *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < cols) row[c + e] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
+    }
 }
 
 template <typename T, bool VEC>
 struct Raw {
-    static constexpr bool PACKED = VEC && sizeof(T) == 2;
+    static constexpr bool PACKED = sizeof(T) == 2;
     static constexpr int N = PACKED ? 4 : 8;     // words: bf16 pairs or floats
     uint32_t w[N];
 
@@ -120,6 +179,8 @@ struct Raw {
                 w[4 * h + 2] = a.z;
                 w[4 * h + 3] = a.w;
             }
+        } else if constexpr (PACKED) {
+            load_run(row + c0 + 8 * lane, cols - c0 - 8 * lane, w);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -135,6 +196,8 @@ struct Raw {
                 const int64_t c = c0 + 8 * lane + 4 * h;
                 if (c < cols) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
             }
+        } else if constexpr (PACKED) {
+            store_run(row + c0 + 8 * lane, cols - c0 - 8 * lane, w);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -152,10 +215,6 @@ struct Raw {
     __device__ __forceinline__ void set(int i, uint64_t v) {
         if constexpr (PACKED) {
             w[i] = sm100::pack_bf16(f2lo(v), f2hi(v));
-        } else if constexpr (sizeof(T) == 2) {
-            const uint32_t b = sm100::pack_bf16(f2lo(v), f2hi(v));
-            w[2 * i] = b << 16;
-            w[2 * i + 1] = b & 0xffff0000u;
         } else {
             w[2 * i] = __float_as_uint(f2lo(v));
             w[2 * i + 1] = __float_as_uint(f2hi(v));
@@ -174,10 +233,10 @@ struct Raw {
 };
 
 // Largest magnitude of each value's group: mag[0] for values 0..3, mag[1] for 4..7.
-template <bool VEC>
+template <bool RUN>
 __device__ __forceinline__ void group_max(const uint64_t* v, uint32_t* mag) {
     uint32_t a = max(magnitude(v[0]), magnitude(v[1])), b = max(magnitude(v[2]), magnitude(v[3]));
-    if (VEC) {                                   // one group in this half warp
+    if (RUN) {                                   // one group in this half warp
         a = max(a, b);
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -193,7 +252,7 @@ __device__ __forceinline__ void group_max(const uint64_t* v, uint32_t* mag) {
 // The fragment's quotients, m[0] / m[1] the divisors of its two halves, as bytes of q's row.
 // q rows are 16-byte aligned; only columns below `cols` are written.  `low`: what is left of each
 // value beyond fp32, or null.
-template <bool VEC>
+template <bool RUN>
 __device__ __forceinline__ void store_e4m3(uint8_t* row, int64_t c0, int64_t cols, int lane, const uint64_t* v,
                                            const float* m, const uint64_t* low = nullptr) {
     auto four = [&](int i, const Divisor& d) {
@@ -203,16 +262,12 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int64_t c0, int64_t col
     const Divisor d0(m[0]);
     const uint32_t lo = four(0, d0);
     uint32_t hi;
-    if (VEC)
+    if (RUN)
         hi = four(2, d0);
     else
         hi = four(2, Divisor(m[1]));
-    if (VEC) {
-        const int64_t c = c0 + 8 * lane;
-        if (c + 8 <= cols)
-            *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);
-        else if (c < cols)                       // fp32 rows end on multiples of 4
-            *reinterpret_cast<uint32_t*>(row + c) = lo;
+    if (RUN) {
+        store_codes(row, c0 + 8 * lane, cols, lo, hi);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -223,13 +278,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int64_t c0, int64_t col
 }
 
 // The scales of the fragment's two groups, from the lanes that own them.
-template <bool VEC>
+template <bool RUN>
 __device__ __forceinline__ void store_scales(float* s, int64_t stride, int64_t c0, int64_t cols, int lane,
                                              const float* sc) {
     const int64_t g = c0 / GROUP;
     if ((lane & 15) == 0) {
         const int h = lane >> 4;
-        if (c0 + GROUP * h < cols) s[(g + h) * stride] = VEC ? sc[0] : sc[h];
+        if (c0 + GROUP * h < cols) s[(g + h) * stride] = RUN ? sc[0] : sc[h];
     }
 }
 
@@ -255,7 +310,7 @@ __device__ __forceinline__ float load_w(const void* w, int bf16, int64_t c) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]) : static_cast<const float*>(w)[c];
 }
 // The weight of a lane's columns, in pairs; zero beyond the row.
-template <bool VEC, int NV>
+template <bool RUN, int NV>
 __device__ __forceinline__ void load_weight(const void* w, int bf16, int64_t cols, int wpr, int part, int lane,
                                             uint64_t (*out)[4]) {
 #pragma unroll
@@ -263,7 +318,7 @@ __device__ __forceinline__ void load_weight(const void* w, int bf16, int64_t col
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t c0 = (int64_t)(i * wpr + part) * 256;
-            const int64_t a = c0 + frag_col<VEC>(lane, 2 * e), b = c0 + frag_col<VEC>(lane, 2 * e + 1);
+            const int64_t a = c0 + frag_col<RUN>(lane, 2 * e), b = c0 + frag_col<RUN>(lane, 2 * e + 1);
             out[i][e] = f2(a < cols ? load_w(w, bf16, a) : 0.f, b < cols ? load_w(w, bf16, b) : 0.f);
         }
 }
@@ -295,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV 
     const int per = (int)(blockDim.x >> 5) / wpr * R, sub = warp / wpr * R;
     const int64_t step = (int64_t)gridDim.x * per;
     uint64_t w[NV][4];
-    load_weight<VEC, NV>(p.w, p.w_bf16, p.cols, wpr, part, lane, w);
+    load_weight<kRun<T, VEC>, NV>(p.w, p.w_bf16, p.cols, wpr, part, lane, w);
     Raw<T, VEC> x[R][NV], res[R][NV];
     auto load = [&](int64_t r) {
 #pragma unroll
@@ -354,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV 
                     n.store(static_cast<T*>(p.n) + row * p.ldn, c0, p.cols, lane);
                 }
                 uint32_t mag[2];
-                group_max<VEC>(u, mag);
+                group_max<kRun<T, VEC>>(u, mag);
                 float m[2], sc[2];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -365,11 +420,11 @@ __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV 
                     uint64_t low[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) low[e] = ffma2(h[k][i].pair(e), w[i][e], u[e] ^ 0x8000000080000000ull);
-                    store_e4m3<VEC>(p.q + row * p.ldq, c0, p.cols, lane, u, m, low);
+                    store_e4m3<kRun<T, VEC>>(p.q + row * p.ldq, c0, p.cols, lane, u, m, low);
                 } else {
-                    store_e4m3<VEC>(p.q + row * p.ldq, c0, p.cols, lane, u, m);
+                    store_e4m3<kRun<T, VEC>>(p.q + row * p.ldq, c0, p.cols, lane, u, m);
                 }
-                store_scales<VEC>(p.scale + row * p.s_row, p.s_grp, c0, p.cols, lane, sc);
+                store_scales<kRun<T, VEC>>(p.scale + row * p.s_row, p.s_grp, c0, p.cols, lane, sc);
             }
         }
     }
@@ -403,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rms_bwd_kerne
     const int rows_b = (int)(blockDim.x >> 5) / wpr, per = rows_b * R, sub = warp / wpr * R;
     const int64_t step = (int64_t)gridDim.x * per;
     uint64_t w[NV][4], dw[NV][4];
-    load_weight<VEC, NV>(p.w, p.w_bf16, p.cols, wpr, part, lane, w);
+    load_weight<kRun<T, VEC>, NV>(p.w, p.w_bf16, p.cols, wpr, part, lane, w);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -424,10 +479,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rms_bwd_kerne
             }
         }
     };
+    constexpr bool AHEAD = THREADS <= 640;       // else the registers do not hold two rows
     int64_t r = (int64_t)blockIdx.x * per + sub;
-    load(r);
+    if (AHEAD) load(r);
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += step, r += step, turn ^= 1) {
+        if (!AHEAD) load(r);
         uint64_t g[R][NV][4], n[R][NV][4], a[R][NV][4];
         float rstd[R], mean[R];
 #pragma unroll
@@ -445,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rms_bwd_kerne
                     a[k][i][e] = p.dh ? dh[k][i].pair(e) : 0;
                 }
         }
-        load(r + step);
+        if (AHEAD) load(r + step);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             uint64_t dot = 0;
@@ -479,8 +536,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rms_bwd_kerne
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                join[(warp * NV + i) * 256 + frag_col<VEC>(lane, 2 * e)] = f2lo(dw[i][e]);
-                join[(warp * NV + i) * 256 + frag_col<VEC>(lane, 2 * e + 1)] = f2hi(dw[i][e]);
+                join[(warp * NV + i) * 256 + frag_col<kRun<T, VEC>>(lane, 2 * e)] = f2lo(dw[i][e]);
+                join[(warp * NV + i) * 256 + frag_col<kRun<T, VEC>>(lane, 2 * e + 1)] = f2hi(dw[i][e]);
             }
         __syncthreads();
         // column c of the row lies with warp (c / 256) % wpr of each row, fragment (c / 256) / wpr
@@ -496,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rms_bwd_kerne
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int64_t c0 = (int64_t)(i * wpr + part) * 256;
-                const int64_t ca = c0 + frag_col<VEC>(lane, 2 * e), cb = c0 + frag_col<VEC>(lane, 2 * e + 1);
+                const int64_t ca = c0 + frag_col<kRun<T, VEC>>(lane, 2 * e), cb = c0 + frag_col<kRun<T, VEC>>(lane, 2 * e + 1);
                 if (ca < p.cols) out[ca] = f2lo(dw[i][e]);
                 if (cb < p.cols) out[cb] = f2hi(dw[i][e]);
             }
@@ -557,37 +614,37 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p)
         for (int e = 0; e < 4; ++e) v[e] = next.pair(e);
         load(t + step);
         uint32_t mag[2];
-        group_max<VEC>(v, mag);
+        group_max<kRun<T, VEC>>(v, mag);
         float m[2], sc[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             m[g] = divisor(mag[g]);
             sc[g] = m[g] * (1.0f / TOP);
         }
-        store_e4m3<VEC>(p.q + r * p.ldq, c0, p.cols, lane, v, m);
-        store_scales<VEC>(p.scale + r * p.s_row, p.s_grp, c0, p.cols, lane, sc);
+        store_e4m3<kRun<T, VEC>>(p.q + r * p.ldq, c0, p.cols, lane, v, m);
+        store_scales<kRun<T, VEC>>(p.scale + r * p.s_row, p.s_grp, c0, p.cols, lane, sc);
     }
 }
 
 // A 128 x 128 tile of x in one block of 512 threads, TC columns x TR rows a thread:
-//   bf16 VEC  8 columns x 4 rows (16-byte loads, 16 lanes a row), kept as loaded
+//   bf16      8 columns x 4 rows (16-byte loads where VEC, 16 lanes a row), kept as loaded
 //   fp32 VEC  4 columns x 8 rows (16-byte loads, a warp a row)
 //   else      columns l + 32j, 8 rows (single loads, a warp a row)
 template <typename T, bool VEC>
 struct Tile {
-    static constexpr bool PACKED = VEC && sizeof(T) == 2;
+    static constexpr bool PACKED = sizeof(T) == 2, RUN = kRun<T, VEC>;
     static constexpr int TC = PACKED ? 8 : 4;
     static constexpr int TR = 32 / TC;
     static constexpr int LPR = 128 / TC;         // lanes a row
     uint32_t v[TR][4];                           // four bf16 pairs or four floats
 
-    static __device__ __forceinline__ int col(int lane, int j) { return VEC ? (lane % LPR) * TC + j : lane + 32 * j; }
+    static __device__ __forceinline__ int col(int lane, int j) { return RUN ? (lane % LPR) * TC + j : lane + 32 * j; }
     static __device__ __forceinline__ int row(int warp, int lane) { return warp * 8 + (lane / LPR) * TR; }
 
     __device__ __forceinline__ void load(const QuantParams& p, int64_t r0, int64_t c0, int warp, int lane) {
         const int64_t r = r0 + row(warp, lane), c = c0 + col(lane, 0);
         const int rows = (int)min((int64_t)TR, p.rows - r);
-        const T* x = static_cast<const T*>(p.x) + r * p.ldx + (VEC ? c : c0);
+        const T* x = static_cast<const T*>(p.x) + r * p.ldx + (RUN ? c : c0);
 #pragma unroll
         for (int i = 0; i < TR; ++i, x += p.ldx) {
             const bool live = i < rows && c < p.cols;
@@ -598,6 +655,8 @@ struct Tile {
                 v[i][1] = w.y;
                 v[i][2] = w.z;
                 v[i][3] = w.w;
+            } else if constexpr (PACKED) {
+                load_run(x, live ? p.cols - c : 0, v[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -612,13 +671,13 @@ struct Tile {
     }
     // Where word w (four rows) of column c lies in the transposed tile: rotated by the lane that
     // writes the column, so that a warp's words, and a column's, meet 32 banks.
-    static __device__ __forceinline__ int owner(int c) { return PACKED ? c >> 3 : VEC ? c >> 2 : c & 31; }
+    static __device__ __forceinline__ int owner(int c) { return PACKED ? c >> 3 : RUN ? c >> 2 : c & 31; }
     static __device__ __forceinline__ int spot(int c, int w) { return c * 32 + (w ^ (PACKED ? 2 * owner(c) : owner(c))); }
     // The divisors of a lane's j-th column pair lie together, those of the lanes side by side: index
     // of column c's float (its M, and two further its 1 / M).
     static __device__ __forceinline__ int pair_at(int lane, int j) { return 4 * (j * LPR + lane % LPR); }
     static __device__ __forceinline__ int divisor_at(int c) {
-        return VEC ? pair_at(owner(c), (c % TC) >> 1) + (c & 1) : pair_at(c & 31, c >> 6) + ((c >> 5) & 1);
+        return RUN ? pair_at(owner(c), (c % TC) >> 1) + (c & 1) : pair_at(c & 31, c >> 6) + ((c >> 5) & 1);
     }
     // Magnitudes as integers that order like them: pairs of 16 bits (PACKED) or one of 32.
     static __device__ __forceinline__ uint32_t mag(uint32_t w) { return w & (PACKED ? 0x7fff7fffu : 0x7fffffffu); }
@@ -765,14 +824,11 @@ __global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !ROWS ? 3 : 2) qu
             uint64_t f[L::TC / 2];
 #pragma unroll
             for (int j = 0; j < L::TC / 2; ++j) f[j] = t.pair(i, j);
-            if constexpr (VEC) {
+            if constexpr (L::PACKED) {
+                store_codes(out, c0 + L::col(lane, 0), p.cols, e4m3x4(f[0], f[1], d), e4m3x4(f[2], f[3], d));
+            } else if constexpr (VEC) {
                 const int64_t c = c0 + L::col(lane, 0);
-                if (c < p.cols) {
-                    if constexpr (L::TC == 8)
-                        *reinterpret_cast<uint2*>(out + c) = make_uint2(e4m3x4(f[0], f[1], d), e4m3x4(f[2], f[3], d));
-                    else
-                        *reinterpret_cast<uint32_t*>(out + c) = e4m3x4(f[0], f[1], d);
-                }
+                if (c < p.cols) *reinterpret_cast<uint32_t*>(out + c) = e4m3x4(f[0], f[1], d);
             } else {
                 const uint32_t b = e4m3x4(f[0], f[1], d);
 #pragma unroll
