@@ -2,7 +2,7 @@
 //   add_rms_norm_kernel   h = x + residual, n = h / rms(h) * weight, n in e4m3
 //                         with one scale per row and 128 channels
 //   rms_bwd_kernel        its gradients (and sum_columns_kernel for d_weight)
-//   quantize_*_kernel     a matrix in e4m3 with 1 x 128 or 128 x 128 scales, as
+//   quantize_tile_kernel  a matrix in e4m3 with 1 x 128 or 128 x 128 scales, as
 //                         it lies or transposed
 //
 // A group whose largest magnitude is m (held at LEAST or above) keeps
@@ -595,37 +595,6 @@ struct QuantParams {
     int64_t st_row, st_grp;
 };
 
-// 1 x 128 groups along the rows: a warp takes 256 columns of a row at a time.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t chunks = (p.cols + 255) / 256, items = p.rows * chunks, step = (int64_t)gridDim.x * 8;
-    int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    Raw<T, VEC> next;
-    auto load = [&](int64_t at) {
-        const int64_t r = at / chunks;
-        next.load(static_cast<const T*>(p.x) + r * p.ldx, (at - r * chunks) * 256, at < items ? p.cols : 0, lane);
-    };
-    load(t);
-    for (; t < items; t += step) {
-        const int64_t r = t / chunks, c0 = (t - r * chunks) * 256;
-        uint64_t v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = next.pair(e);
-        load(t + step);
-        uint32_t mag[2];
-        group_max<kRun<T, VEC>>(v, mag);
-        float m[2], sc[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            m[g] = divisor(mag[g]);
-            sc[g] = m[g] * (1.0f / TOP);
-        }
-        store_e4m3<kRun<T, VEC>>(p.q + r * p.ldq, c0, p.cols, lane, v, m);
-        store_scales<kRun<T, VEC>>(p.scale + r * p.s_row, p.s_grp, c0, p.cols, lane, sc);
-    }
-}
-
 // A 128 x 128 tile of x in one block of 512 threads, TC columns x TR rows a thread:
 //   bf16      8 columns x 4 rows (16-byte loads where VEC, 16 lanes a row), kept as loaded
 //   fp32 VEC  4 columns x 8 rows (16-byte loads, a warp a row)
@@ -693,12 +662,14 @@ struct Tile {
 };
 
 // 128 x 128 blocks (SQUARE), or 1 x 128 groups along the columns for q and along the rows for the
-// transpose.  ROWS writes q, TRANSPOSE the transpose, through shared memory.  The transposing form is
+// transpose.  ROWS writes q, TRANSPOSE the transpose, through shared memory.  ROWS alone, in 1 x 128
+// groups, needs neither shared memory nor a barrier (40000 x 1000 in bf16: 28 us; a warp for 256
+// columns of a row at a time took 51).  The transposing form is
 // bound by its instructions (15 a value; 131072 x 1024 in bf16: 85 us, 63 at the copy's rate): column
 // pairs go through the quotient together, three blocks an SM (bf16) cover each other's barriers.
 // Walking the tiles with the next one on its way in registers took 115 us, for the blocks it costs.
 template <typename T, bool VEC, bool SQUARE, bool ROWS, bool TRANSPOSE>
-__global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !ROWS ? 3 : 2) quantize_tile_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !(ROWS && TRANSPOSE) ? 3 : 2) quantize_tile_kernel(const QuantParams p) {
     using L = Tile<T, VEC>;
     constexpr int W = L::PACKED ? 64 : 128;      // words of a warp's column maxima
     constexpr bool BY_COL = TRANSPOSE && !SQUARE;
