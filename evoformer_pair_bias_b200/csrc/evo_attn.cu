@@ -31,7 +31,7 @@
 #include "fp8_rows.cuh"
 #include "fp8_sm100.cuh"
 
-#define EVO_VERSION 10000
+#define EVO_VERSION 10100
 
 namespace {
 

@@ -240,6 +240,36 @@ def test_add_rms_norm_zero_rows_nan_rows_and_least_maximum():
     assert s[[2, 3]].isnan().all()
 
 
+def test_rows_off_16_bytes_and_their_neighbours():
+    # bf16 rows at even and odd element offsets inside wider ones: the values beside them are NaN
+    # on the way in, and on the way out they stay as they were
+    g = gen(20)
+    lib = A.load_library()
+    for cols in (1, 7, 8, 9, 255, 263, 1001):
+        for off in range(4):
+            for pitch in (cols + 5, (cols + 15) // 8 * 8):
+                wide = torch.full((6, pitch + 8), float("nan"), dtype=BF16, device="cuda")
+                x = wide[:, off:off + cols]
+                x.copy_(stream_rows(6, cols, g, BF16))
+                want = fp8.add_rms_norm_fp8(x.contiguous(), x.contiguous(), None, 1e-5, want_n=True)
+                h_buf = torch.full((6, pitch + 8), 5.0, dtype=BF16, device="cuda")
+                n_buf = h_buf.clone()
+                q, s = fp8.empty_codes(6, cols, x.device), fp8.empty_scales(6, -(-cols // 128), x.device)
+                at = lambda b: b.data_ptr() + 2 * off  # noqa: E731
+                rc = lib.evo_add_rms_norm_fp8(6, cols, 0, at(wide), pitch + 8, at(wide), pitch + 8, None, 0, 1e-5,
+                                              A._ptr(q), q.stride(0), A._ptr(s), 1, 6, at(h_buf), pitch + 8, at(n_buf),
+                                              pitch + 8, None, A._stream(x.device))
+                assert rc == 0
+                for buf, ref in ((h_buf, want[2]), (n_buf, want[4])):
+                    assert torch.equal(buf[:, off:off + cols], ref)
+                    assert (buf[:, :off] == 5).all() and (buf[:, off + cols:] == 5).all()
+                assert torch.equal(q.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(s, want[1])
+                for kw in ({}, {"transpose": True}, {"square": True}):
+                    for a, b in zip(fp8.quantize_fp8(x, **kw), fp8.quantize_fp8(x.contiguous(), **kw)):
+                        assert torch.equal(a.view(torch.uint8) if a.dtype == fp8.CODES else a,
+                                           b.view(torch.uint8) if b.dtype == fp8.CODES else b)
+
+
 def test_add_rms_norm_in_place_on_the_residual_stream():
     # h may be x or the residual itself: the C call, with the rows of both pitches
     g = gen(21)
@@ -376,7 +406,7 @@ def test_fp8_linear_scale_layouts_pitches_and_untouched_bytes():
         wide[:, 16:16 + K] = xq.contiguous().view(torch.uint8)
         xw = wide.view(fp8.CODES)[:, 16:16 + K]
         assert torch.equal(want, fp8.fp8_linear(xw, xs, wq, ws))
-        for off, ld in ((0, N + 8), (1, N + 3)):
+        for off, ld in ((0, N + 8), (1, N + 3)):         # the second: rows at odd addresses
             buf = torch.full((M + 1, ld), 9.0, dtype=BF16, device="cuda")
             rc = lib.evo_fp8_linear(M, N, K, A._ptr(xq), xq.stride(0), A._ptr(xs), xs.stride(0), xs.stride(1),
                                     A._ptr(wq), wq.stride(0), A._ptr(ws), ws.stride(0), ws.stride(1), 0, None, 0,
@@ -592,6 +622,54 @@ def test_graph_replay_matches_eager():
         graph.replay()
         for a, b in zip(got, step()):
             assert torch.equal(a, b)
+
+
+def test_captured_training_step_matches_eager():
+    # the capture has leaves of its own: no eager graph of them is alive beside it
+    g = gen(72)
+    data = [randn(s, g, BF16) for s in ((130, 200), (130, 200), (200,), (96, 200))]
+    dh, dy = randn((130, 200), g, BF16), randn((130, 96), g, BF16)
+
+    def step(leaves):
+        h, y = fp8.add_rms_norm_linear(leaves[0], leaves[1], leaves[2], 1e-5, leaves[3])
+        return (h, y) + torch.autograd.grad((h, y), leaves, (dh, dy))
+
+    want = [t.detach().clone() for t in step([t.clone().requires_grad_(True) for t in data])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step([t.clone().requires_grad_(True) for t in data])
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    leaves = [t.clone().requires_grad_(True) for t in data]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(leaves)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_two_captured_products_keep_their_own_workspaces():
+    g = gen(74)
+    sets = [operands(8, 512, 16384, True, g) for _ in range(2)]
+    want = [fp8.fp8_linear(*s) for s in sets]
+    graphs, got = [], []
+    for s in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(fp8.fp8_linear(*s))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_calls_on_two_streams_do_not_disturb_each_other():
