@@ -27,11 +27,13 @@ from .attention import DTYPES, EVO_OK, EvoError, _opt_f32, load_library
 
 GROUP = 128
 CODES = torch.float8_e4m3fn
+EVO_ERR_WORKSPACE_TOO_SMALL = 3
 
 # A call costs the host some ten microseconds, as much as the smaller kernels take on the
 # GPU: the functions below avoid objects where a number will do (addresses and the raw
 # stream go to ctypes as integers) and ask each tensor once.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _empty = torch.empty_strided
 
 
@@ -54,15 +56,18 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(where, dev, *args):
-    """One library call with `dev` current, on its current stream."""
+def _status(where, dev, *args):
+    """The status of one library call with `dev` current, on its current stream."""
     fn = getattr(load_library(), where)
     i = dev.index
-    if i == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(i):
-            rc = fn(*args, _raw_stream(i))
+    if i == _current_device():
+        return fn(*args, _raw_stream(i))
+    with torch.cuda.device(i):
+        return fn(*args, _raw_stream(i))
+
+
+def _call(where, dev, *args):
+    rc = _status(where, dev, *args)
     if rc != EVO_OK:
         raise EvoError(where, rc)
 
@@ -287,11 +292,16 @@ def fp8_linear(xq, x_scale, wq, w_scale, bias=None, out_dtype=torch.bfloat16):
     y = _empty((M, N), (N, 1), dtype=out_dtype, device=dev)
     if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
         bias = _opt_f32(bias, N, dev)
-    nbytes, ws = load_library().evo_fp8_linear_workspace_bytes(M, N, K), None
-    if nbytes:
+    args = (M, N, K, x_at, ldx, xs.data_ptr(), sxr, sxg, w_at, ldw, w_scale.data_ptr(), swr, swg, sn != blocks,
+            _addr(bias), DTYPES[out_dtype], y.data_ptr(), N)
+    # most sizes need no workspace: a call without one is refused before anything is enqueued
+    rc = _status("evo_fp8_linear", dev, *args, None, 0)
+    if rc == EVO_ERR_WORKSPACE_TOO_SMALL:
+        nbytes = load_library().evo_fp8_linear_workspace_bytes(M, N, K)
         ws = _empty((nbytes // 4,), (1,), dtype=torch.float32, device=dev)
-    _call("evo_fp8_linear", dev, M, N, K, x_at, ldx, xs.data_ptr(), sxr, sxg, w_at, ldw, w_scale.data_ptr(), swr, swg,
-          sn != blocks, _addr(bias), DTYPES[out_dtype], y.data_ptr(), N, _addr(ws), nbytes)
+        rc = _status("evo_fp8_linear", dev, *args, ws.data_ptr(), nbytes)
+    if rc != EVO_OK:
+        raise EvoError("evo_fp8_linear", rc)
     return y if len(lead) == 1 else y.view(*lead, N)
 
 
