@@ -515,7 +515,7 @@ evo_status_t launch_linear_as(const evo::fp8::LinParams& p, int S, cudaStream_t 
         cudaFuncAttributes fa{};
         return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
     }();
-    if (regs != f8::LAUNCH_REGS) return EVO_ERR_CUDA;
+    if (regs != L::LAUNCH_REGS) return EVO_ERR_CUDA;
     const int64_t tm = (p.M + f8::BM - 1) / f8::BM;
     const int64_t tiles = tm * ((p.N + L::BN - 1) / L::BN) * (L::PART ? p.parts : 1);
     if (tiles * S > 0x7fffffff - 65536) return EVO_ERR_UNSUPPORTED;
@@ -530,7 +530,7 @@ evo_status_t launch_linear_as(const evo::fp8::LinParams& p, int S, cudaStream_t 
         return EVO_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(L::JOIN ? tiles * S : std::min<int64_t>(tiles, sm_count())));
-    cfg.blockDim = dim3(f8::THREADS);
+    cfg.blockDim = dim3(L::THREADS);
     cfg.dynamicSmemBytes = L::smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
@@ -559,7 +559,7 @@ struct LinPlan {
 // rows 23.4 and 23.3; four 34.9 and 24).  Else the costs are in blocks of 128 x 256 x 128 on one SM
 // (0.6 us): a block of 128 columns takes as long as one of 256 (both wait more than they add), a
 // CTA's start, last step and end about five, a second launch with its pass over the parts four more.
-// Measured both ways: 1024 x 131072 x 256 takes 99 us in clusters of 6, 60 in parts.
+// Measured both ways: 1024 x 131072 x 256 takes 99 us in clusters of 6, 57 in parts.
 LinPlan plan_linear(int64_t M, int64_t N, int64_t K) {
     namespace f8 = evo::fp8;
     // clusters of 1 to 8 CTAs that run at once on 148 SMs (a cluster lies in one GPC)
@@ -606,7 +606,9 @@ template <typename T, bool SW_ROWS>
 evo_status_t launch_linear(const evo::fp8::LinParams& p, const LinPlan& plan, void* workspace, cudaStream_t stream) {
     namespace f8 = evo::fp8;
     if (plan.form == LinPlan::FEW) return launch_linear_few<T, SW_ROWS>(p, plan.S, stream);
-    if (plan.form == LinPlan::WIDE) return launch_linear_as<T, SW_ROWS, f8::Wide>(p, 1, stream);
+    if (plan.form == LinPlan::WIDE)                        // both sides are measured beside linear_kernel
+        return p.K > 8 * f8::BK ? launch_linear_as<T, SW_ROWS, f8::Long>(p, 1, stream)
+                                : launch_linear_as<T, SW_ROWS, f8::Wide>(p, 1, stream);
     if (plan.form == LinPlan::SPLIT) return launch_linear_as<T, SW_ROWS, f8::Split>(p, plan.S, stream);
     f8::LinParams parts = p;
     parts.y = workspace;

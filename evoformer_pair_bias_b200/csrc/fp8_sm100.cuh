@@ -79,8 +79,8 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 // ------------------------------------------------------------------ the kernel
 // One CTA per SM, tiles of 128 x BN of y.  Roles: warp 0 TMA, warp 1 MMA, warp 2 the
 // scales of the coming blocks and warp 3 the bias of the coming tile (cp.async into
-// shared memory), warps 4-19 add up the blocks (warp % 4: the quarter of TMEM lanes a
-// warp may read; (warp - 4) / 4: its quarter of the columns) and write the tile.
+// shared memory), the warps from 4 on add up the blocks (warp % 4: the quarter of TMEM
+// lanes a warp may read; (warp - 4) / 4: its share of the columns) and write the tile.
 //
 // Wide   256 columns, persistent: the tiles of a row block in succession.  While one is
 //        written the next one's first two blocks are multiplied.  y leaves through
@@ -97,18 +97,25 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 //
 // The summing warps are what bounds the long sums: a block's 128 x BN results are read
 // from TMEM and added in the time the tensor core takes for the next (512 cycles at BN =
-// 256).  Sixteen warps of 64 columns hide each other's waits and share a tile's way out:
-// 131072 x 256 x 1024 takes 63 us, 8191 x 4096 x 8192 takes 260 (the MMAs and loads alone:
-// 180); eight of 128 columns need fewer instructions and take 71 and 250.  They hold their
-// sums and nothing that comes from global memory: scales and bias fetched into their own
-// registers spilled and waited for the load at the spill (125 us and 350).
-constexpr int SUM_WARPS = 16;                              // 4 column groups x 4 lane quarters
-constexpr int THREADS = 32 * (4 + SUM_WARPS);
+// 256).  Sixteen warps of 64 columns share a tile's way out best: 131072 x 256 x 1024
+// takes 63 us, 71 with eight.  Eight of 128 columns hold twice the registers and need
+// fewer instructions a block: 8191 x 4096 x 8192 takes 301 us back to back under the power
+// cap, 315 with sixteen; 16384 x 1280 x 4096 95 and 98.5; at a sum of 1024 the two are
+// equal (82 us), so that is where Long begins.  The warps hold their sums and nothing that
+// comes from global memory: scales and bias fetched into their own registers spilled and
+// waited for the load at the spill (125 us and 350).
 constexpr int RING = 8;                                    // blocks whose scales are held
 enum Mode { WHOLE, JOINED, PARTS };
-template <int BN_, int STAGES_, Mode MODE>
+template <int BN_, int STAGES_, Mode MODE, int WARPS>
 struct Config {
     static constexpr int BN = BN_, STAGES = STAGES_;
+    static constexpr int SUM_WARPS = WARPS;                // column groups x 4 lane quarters
+    static constexpr int THREADS = 32 * (4 + SUM_WARPS);
+    // registers per thread: at launch, and as handed from the control warps to the others
+    static constexpr int LAUNCH_REGS = WARPS == 16 ? 96 : 168;
+    static constexpr int CTRL_REGS = WARPS == 16 ? 32 : 56, SUM_REGS = WARPS == 16 ? 112 : 216;
+    static_assert(4 * CTRL_REGS + SUM_WARPS * SUM_REGS <= (4 + SUM_WARPS) * LAUNCH_REGS, "register split");
+    static_assert(LAUNCH_REGS * THREADS <= 65536, "registers of an SM");
     static constexpr bool JOIN = MODE == JOINED;           // a cluster's CTAs join one tile
     static constexpr bool PART = MODE == PARTS;            // each item sums a run of blocks into the workspace
     static constexpr int GROUPS = JOIN ? 2 : 1;            // groups of summing warps, which take the blocks in turn
@@ -117,9 +124,10 @@ struct Config {
     static constexpr int BUFS = 512 / BN;                  // blocks' results in TMEM
     static constexpr int STAGE_BYTES = (BM + BN) * BK;
     static constexpr int SLOT = (BM + BN) * 4;             // 128 scales of x, then BN / 128 or BN of w
-    static constexpr int BOX = 32 * 128;                   // JOIN: the tile lies over the stages instead
+    static constexpr int BOX = 32 * 128, BOXES = 16 / WARPS;   // of a warp; JOIN: the tile lies over the stages instead
+    static constexpr int READ = WARPS == 16 ? 32 : 64;     // columns read from TMEM at a time
     static constexpr int stg_off = STAGES * STAGE_BYTES;
-    static constexpr int ring_off = stg_off + (JOIN ? 0 : SUM_WARPS * BOX);
+    static constexpr int ring_off = stg_off + (JOIN ? 0 : SUM_WARPS * BOXES * BOX);
     static constexpr int bias_off = ring_off + RING * SLOT;
     static constexpr int bar_off = bias_off + 2 * BN * 4;
     static constexpr int n_bars = 2 * STAGES + 2 * RING + 2 * BUFS + 5;
@@ -128,12 +136,10 @@ struct Config {
     static_assert(smem <= 232448, "shared memory budget");
     static_assert(!JOIN || (BN == 128 && stg_off >= GROUPS * BM * BN * 4), "the groups' tiles lie over the stages");
 };
-using Wide = Config<256, 3, WHOLE>;
-using Split = Config<128, 6, JOINED>;
-using Parts = Config<256, 3, PARTS>;
-// registers per thread: 96 at launch (20 warps), handed from the control warps to the others
-constexpr int LAUNCH_REGS = 96, CTRL_REGS = 32, SUM_REGS = 112;
-static_assert(4 * CTRL_REGS + SUM_WARPS * SUM_REGS <= (4 + SUM_WARPS) * LAUNCH_REGS, "register split");
+using Wide = Config<256, 3, WHOLE, 16>;
+using Long = Config<256, 3, WHOLE, 8>;                     // Wide, for sums of more than 1024
+using Split = Config<128, 6, JOINED, 16>;
+using Parts = Config<256, 3, PARTS, 8>;
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -154,7 +160,7 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int ch) {
 }
 
 template <typename T, bool SW_ROWS, class L>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(L::THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                   const __grid_constant__ CUtensorMap tm_y, const LinParams p, const int tma_out) {
     extern __shared__ uint8_t smem_raw[];
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_bfull(b), 32);
-            mbar_init(bar_bempty(b), SUM_WARPS);
+            mbar_init(bar_bempty(b), L::SUM_WARPS);
         }
         mbar_init(bar_done, 1);
         *abort_flag = 0;
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
-        regs_decrease<CTRL_REGS>();
+        regs_decrease<L::CTRL_REGS>();
         bool ok = true;
         uint32_t n = 0;
         if (warp == 0 && lane == 0) {
@@ -316,10 +322,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             cp_async_wait_all();
         }
     } else {
-        regs_increase<SUM_REGS>();
+        regs_increase<L::SUM_REGS>();
         // this warp's lanes and columns of the tile, and its group
         const int quarter = warp & 3, col_w = ((warp - 4) % L::GROUP_WARPS >> 2) * COLS, group = (warp - 4) / L::GROUP_WARPS;
-        const uint32_t box = base + L::stg_off + (uint32_t)(warp - 4) * L::BOX;
+        const uint32_t boxes = base + L::stg_off + (uint32_t)(warp - 4) * L::BOXES * L::BOX;
         if (!L::JOIN && lane == 0) prefetch_tmap(&tm_y);
         bool ok = true;
         uint32_t n = (uint32_t)group, tile_no = 0;
@@ -375,16 +381,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 } else {
+                    constexpr int W = L::READ;
 #pragma unroll
-                    for (int c = 0; c < COLS / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32_sync(ta + 32 * c, v);
-                        if (c == COLS / 32 - 1) release();
+                    for (int c = 0; c < COLS / W; ++c) {
+                        uint32_t v[W];
+                        if constexpr (W == 64)
+                            tmem_ld32x2_sync(ta + W * c, ta + W * c + 32, v);
+                        else
+                            tmem_ld32_sync(ta + W * c, v);
+                        if (c == COLS / W - 1) release();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
+                        for (int i = 0; i < W; i += 4) {
                             const uint64_t t0 = f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                             const uint64_t t1 = f2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-                            uint64_t* a = acc + 16 * c + i / 2;
+                            uint64_t* a = acc + (W * c + i) / 2;
                             a[0] = ffma2(t0, f2v, a[0]);
                             a[1] = ffma2(t1, f2v, a[1]);
                         }
@@ -420,14 +430,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
             }
             // chunk `ch` of row `r` in a box, as TMA's 128-byte swizzle places it
+            uint32_t box = boxes;
             auto place = [&](int r, int ch) {
                 return box + r * 128 + ((ch ^ (r & 7)) << 4);
             };
 #pragma unroll
             for (int g = 0; g < COLS / CPB; ++g) {
                 const int c0 = col0 + g * CPB;
+                box = boxes + (uint32_t)(g % L::BOXES) * L::BOX;
                 if (tma_out) {
-                    if (lane == 0) bulk_wait_read<0>();    // the store that last read the box is done with it
+                    if (lane == 0) bulk_wait_read<L::BOXES - 1>();   // the store that last read the box is done with it
                     __syncwarp();
                 }
 #pragma unroll
@@ -459,9 +471,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (tma_out) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && row0 < p.M && c0 < p.N) {
-                        tma_store_2d(&tm_y, box, c0, out0);
-                        bulk_commit();
+                    if (lane == 0) {
+                        if (row0 < p.M && c0 < p.N) tma_store_2d(&tm_y, box, c0, out0);
+                        bulk_commit();                     // also of nothing, so that the wait above keeps its distance
                     }
                 } else {
                     __syncwarp();
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int rows = min(BM, p.M - m0);
         T* y = static_cast<T*>(p.y);
         const bool vec = (p.M == 1 || p.ldy % 4 == 0) && (reinterpret_cast<uintptr_t>(p.y) & (4 * sizeof(T) - 1)) == 0;
-        for (int idx = rank * THREADS + (int)threadIdx.x; idx < rows * 32; idx += S * THREADS) {
+        for (int idx = rank * L::THREADS + (int)threadIdx.x; idx < rows * 32; idx += S * L::THREADS) {
             const int r = idx >> 5, ch = idx & 31, c = n0 + 4 * ch;
             if (c >= p.N) continue;
             const uint32_t at = tile_addr(base, r, ch);

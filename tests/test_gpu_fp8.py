@@ -420,6 +420,29 @@ def test_fp8_linear_scale_layouts_pitches_and_untouched_bytes():
             assert (flat[mask] == 9.0).all()
 
 
+@pytest.mark.parametrize("square", [True, False])
+@pytest.mark.parametrize("M,N,K", [(2500, 2056, 1024), (2500, 2056, 1025), (2049, 2571, 1700)])
+def test_fp8_linear_long_sums_bias_and_odd_pitches(M, N, K, square):
+    # both sides of the sum where whole tiles change their summing warps
+    g = gen(M + N + K)
+    xq, xs, wq, ws = operands(M, N, K, square, g)
+    bias = randn((N,), g)
+    lib = A.load_library()
+    for dtype in (BF16, F32):
+        y = fp8.fp8_linear(xq, xs, wq, ws, bias, out_dtype=dtype)
+        check_linear(y, xq, xs, wq, ws, bias)
+        ld = N + 3
+        buf = torch.full((M * ld + 1,), 9.0, dtype=dtype, device="cuda")
+        rc = lib.evo_fp8_linear(M, N, K, A._ptr(xq), xq.stride(0), A._ptr(xs), xs.stride(0), xs.stride(1),
+                                A._ptr(wq), wq.stride(0), A._ptr(ws), ws.stride(0), ws.stride(1), int(not square),
+                                A._ptr(bias), int(dtype == F32), buf.data_ptr() + buf.element_size(), ld, None, 0,
+                                A._stream(xq.device))
+        assert rc == 0
+        assert torch.equal(torch.as_strided(buf, (M, N), (ld, 1), 1), y)
+        torch.as_strided(buf, (M, N), (ld, 1), 1).fill_(9.0)
+        assert (buf == 9.0).all()
+
+
 def test_fp8_linear_nan_scales_reach_their_rows_only():
     g = gen(43)
     x = randn((300, 260), g, BF16)
