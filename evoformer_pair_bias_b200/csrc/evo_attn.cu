@@ -414,12 +414,17 @@ void by_type(evo_dtype_t dtype, bool vec, F f) {
     dtype == EVO_DTYPE_BF16 ? with(__nv_bfloat16{}) : with(float{});
 }
 
-template <typename T, bool VEC, int NV, int R, int THREADS>
-void launch_norm_as(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {
-    auto kern = evo::fp8::add_rms_norm_kernel<T, VEC, NV, R, THREADS>;
+template <typename T, bool VEC, int NV, int R, int THREADS, bool SMALL>
+void launch_norm_eps(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {
+    auto kern = evo::fp8::add_rms_norm_kernel<T, VEC, NV, R, THREADS, SMALL>;
     static Resident kept;
     const int grid = walking_grid(kern, s.threads, p.rows, s.threads / 32 / s.wpr * R, kept);
     kern<<<grid, s.threads, 0, stream>>>(p, s.wpr);
+}
+template <typename T, bool VEC, int NV, int R, int THREADS>
+void launch_norm_as(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {
+    if (p.eps < 0x1p-20f) return launch_norm_eps<T, VEC, NV, R, THREADS, true>(p, s, stream);
+    return launch_norm_eps<T, VEC, NV, R, THREADS, false>(p, s, stream);
 }
 template <typename T, bool VEC>
 void launch_norm(const evo::fp8::NormParams& p, const RowSplit& s, cudaStream_t stream) {

@@ -15,7 +15,9 @@
 // 7 * 64, so v = 3m/2^k is one); a plain product with 1/m would break them
 // either way.  t is exact for bf16 v and cannot overflow, and neither M nor inv
 // leaves the normal range.  In the norm the row's 1 / rms cancels out of v / m,
-// so the quotient is that of u = h * weight, exact in fp32 for bf16.
+// so the quotient is that of u = h * weight, exact in fp32 for bf16; its least
+// maximum is LEAST * rms, and rows of a rms so small that its M would be
+// subnormal are taken up by a power of two first.
 //
 // All of these move each byte once and are bound by HBM, next to it by the
 // instructions: at 6.4 TB/s an SM has some 17 issue slots a value, so sums and
@@ -342,7 +344,11 @@ __device__ __forceinline__ float row_sum(float v, int wpr, int warp, int first, 
 // worked on: at 32 warps of one row an SM has 32 KB on its way, too little for HBM's latency
 // (196608 x 256 in bf16: 104 us; two rows a warp and the loads ahead 65, with three blocks an SM
 // 61.5, of 54.9 at the copy's rate).
-template <typename T, bool VEC, int NV, int R, int THREADS>
+//
+// SMALL, for eps below 2^-20: rows may have a smaller rms than 2^-10.  They go up by the power of two
+// that leaves the rms at (1/2, 1]: exact, and u and its divisors, down to 2^-100 / 512 of the rms, stay
+// in the normal range.  Any row times a factor takes 65 us there, so a larger eps does without.
+template <typename T, bool VEC, int NV, int R, int THREADS, bool SMALL>
 __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV <= 2 ? 2 : 1) add_rms_norm_kernel(const NormParams p, const int wpr) {
     __shared__ float buf[2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -368,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV 
     // every warp makes the same number of turns, for the barrier in row_sum
     for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += step, r += step, turn ^= 1) {
         Raw<T, VEC> h[R][NV];
-        float rstd[R], least[R], per_m[R];
+        float rstd[R], up[R], rs[R], least[R], per_m[R];
 #pragma unroll
         for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -386,8 +392,15 @@ __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV 
                 for (int e = 0; e < 4; ++e) sq = ffma2(h[k][i].pair(e), h[k][i].pair(e), sq);
             const float ms = row_sum(f2lo(sq) + f2hi(sq), wpr, warp, first, buf[turn]) * p.inv_cols + p.eps;
             rstd[k] = rsqrtf(ms);
-            least[k] = LEAST * ms * rstd[k];               // LEAST / rstd: the least maximum of u = n / rstd
-            per_m[k] = least[k] == least[k] ? rstd[k] * (1.0f / TOP) : least[k];   // NaN where ms is 0 or infinite
+            up[k] = 1.f;                                   // the row's factor, and what it leaves of 1 / rms
+            rs[k] = rstd[k];
+            if (SMALL) {
+                const uint32_t e = min(max(__float_as_uint(rstd[k]) & 0x7f800000u, 0x3f800000u), 0x7e800000u);
+                up[k] = __uint_as_float(e);
+                rs[k] *= __uint_as_float(0x7f000000u - e); // 1 / up
+            }
+            least[k] = LEAST * (ms * rstd[k] * up[k]);     // LEAST / rs: the least maximum of u = n / rs
+            per_m[k] = least[k] == least[k] ? rs[k] * (1.0f / TOP) : least[k];     // NaN where ms is 0 or infinite
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -399,13 +412,17 @@ __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV 
                 const int64_t c0 = (int64_t)(i * wpr + part) * 256;
                 if (c0 >= p.cols) break;
                 if (p.h) h[k][i].store(static_cast<T*>(p.h) + row * p.ldh, c0, p.cols, lane);
-                uint64_t u[4];
+                uint64_t v[4], u[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = fmul2(h[k][i].pair(e), w[i][e]);
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = h[k][i].pair(e);
+                    if (SMALL) v[e] = fmul2(v[e], twice(up[k]));
+                    u[e] = fmul2(v[e], w[i][e]);
+                }
                 if (p.n) {
                     Raw<T, VEC> n;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) n.set(e, fmul2(u[e], twice(rstd[k])));
+                    for (int e = 0; e < 4; ++e) n.set(e, fmul2(u[e], twice(rs[k])));
                     n.store(static_cast<T*>(p.n) + row * p.ldn, c0, p.cols, lane);
                 }
                 uint32_t mag[2];
@@ -419,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, THREADS != 256 ? 1 : R == 2 ? 3 : NV 
                 if constexpr (sizeof(T) == 4) {            // fp32: u is rounded, its rest goes into the quotient
                     uint64_t low[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) low[e] = ffma2(h[k][i].pair(e), w[i][e], u[e] ^ 0x8000000080000000ull);
+                    for (int e = 0; e < 4; ++e) low[e] = ffma2(v[e], w[i][e], u[e] ^ 0x8000000080000000ull);
                     store_e4m3<kRun<T, VEC>>(p.q + row * p.ldq, c0, p.cols, lane, u, m, low);
                 } else {
                     store_e4m3<kRun<T, VEC>>(p.q + row * p.ldq, c0, p.cols, lane, u, m);

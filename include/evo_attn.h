@@ -344,8 +344,9 @@ evo_status_t evo_sum_partials(int64_t count, const float* const* parts, int64_t 
  * NULL.  Statistics and products are fp32; n is quantised before it is
  * rounded to `dtype`.  In the norm the group maximum that is held at 2^-100
  * is that of n.  A row whose sum of squares overflows fp32 comes out with NaN
- * scales.  1 <= cols <= 32768 (EVO_ERR_UNSUPPORTED above); rows == 0 is a
- * no-op.
+ * scales, and so does, with eps == 0, one whose mean of squares is 0 in fp32
+ * (rms below 2^-75, zero rows among them; below 2^-63 rstd loses digits).
+ * 1 <= cols <= 32768 (EVO_ERR_UNSUPPORTED above); rows == 0 is a no-op.
  */
 evo_status_t evo_add_rms_norm_fp8(int64_t rows, int64_t cols, evo_dtype_t dtype, const void* x, int64_t ldx,
                                   const void* residual, int64_t ldr, const void* weight, evo_dtype_t w_dtype,
