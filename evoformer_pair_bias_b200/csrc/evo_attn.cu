@@ -1071,6 +1071,12 @@ evo_status_t evo_quantize_fp8_both(int64_t rows, int64_t cols, evo_dtype_t dtype
     return quantize(p, dtype, square != 0, static_cast<cudaStream_t>(stream));
 }
 
+// Zeros in rows x cols elements of e bytes at a pitch of ld elements.
+static bool zero_matrix(void* p, int64_t rows, int64_t cols, int64_t ld, int64_t e, void* stream) {
+    return cudaMemset2DAsync(p, (size_t)((rows > 1 ? ld : cols) * e), 0, (size_t)(cols * e), (size_t)rows,
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess;
+}
+
 // Where evo_fp8_linear_bwd keeps its operands in the workspace.
 struct BwdOperands {
     int64_t ld_n, ld_m;          // pitches of dy's codes, and of both transposes
@@ -1141,14 +1147,19 @@ evo_status_t evo_fp8_linear_bwd(int64_t M, int64_t N, int64_t K, evo_dtype_t dty
                                 evo_dtype_t dw_dtype, int64_t lddw, void* workspace, size_t workspace_bytes,
                                 void* stream) {
     if (M < 0 || N < 0 || K < 1 || !dtype_ok(dtype) || !dtype_ok(dw_dtype)) return EVO_ERR_INVALID_ARG;
-    if (N == 0 || (!dx && !dw)) return EVO_OK;
+    if (!dx && !dw) return EVO_OK;
     if (dw && N > 1 && lddw < K) return EVO_ERR_INVALID_ARG;
-    if (M == 0) {                                           // the empty sum
-        const size_t e = (size_t)elem_bytes(dw_dtype);
-        if (dw && cudaMemset2DAsync(dw, (size_t)(N > 1 ? lddw : K) * e, 0, (size_t)K * e, (size_t)N,
-                                    static_cast<cudaStream_t>(stream)) != cudaSuccess)
-            return EVO_ERR_CUDA;
-        return EVO_OK;
+    if (M == 0 || N == 0) {                                 // the empty sums: dw without rows, dx without outputs
+        if (dw && N > 0 && !zero_matrix(dw, N, K, lddw, elem_bytes(dw_dtype), stream)) return EVO_ERR_CUDA;
+        if (!dx || M == 0) return EVO_OK;
+        if ((M > 1 && lddx < K) || !aligned(dx, elem_bytes(dtype))) return EVO_ERR_INVALID_ARG;
+        // a dx that the runtime does not know (where there is no device, none is known) is not written
+        cudaPointerAttributes at{};
+        if (cudaPointerGetAttributes(&at, dx) != cudaSuccess || at.type == cudaMemoryTypeUnregistered) {
+            cudaGetLastError();
+            return EVO_OK;
+        }
+        return zero_matrix(dx, M, K, lddx, elem_bytes(dtype), stream) ? EVO_OK : EVO_ERR_CUDA;
     }
     if (M > kMaxProduct || N > kMaxProduct || K > kMaxProduct) return EVO_ERR_UNSUPPORTED;
     if (!dy || (dw && !x) || (dx && (!w_t || !w_t_scale)) || (dx && M > 1 && lddx < K)) return EVO_ERR_INVALID_ARG;

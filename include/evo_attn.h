@@ -440,8 +440,8 @@ evo_status_t evo_fp8_linear(int64_t M, int64_t N, int64_t K, const void* x, int6
  *
  * x may be NULL without dw, w_t and its scales without dx.  workspace: at
  * least evo_fp8_linear_bwd_workspace_bytes(M, N, K, dx, dw) bytes, 256-byte
- * aligned, contents arbitrary; calls that may overlap need one each.  M == 0
- * sets dw to zero.
+ * aligned, contents arbitrary; calls that may overlap need one each.  K >= 1;
+ * M == 0 sets dw to zero, N == 0 sets dx to zero.
  */
 size_t evo_fp8_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int want_dx, int want_dw);
 evo_status_t evo_fp8_linear_bwd(int64_t M, int64_t N, int64_t K, evo_dtype_t dtype, const void* dy, int64_t lddy,

@@ -73,3 +73,53 @@ def test_projection_of_zero_rows_is_zero_for_any_eps(dtype):
     for eps in (1e-5, 1e-12, 1e-16, 1e-30):
         h, y = fp8.add_rms_norm_linear(x, None, gamma, eps, w)
         assert (y[[1, 4]] == 0).all() and torch.isfinite(y).all() and (y[[0, 2, 3]] != 0).any(1).all()
+
+
+# ------------------------------------------------------------------- empty axes
+def leave_nans(*shapes, dtype=BF16):
+    """Memory that the next results of these shapes may get, full of NaN."""
+    for s in shapes:
+        for t in [torch.full(s, float("nan"), dtype=dtype, device="cuda") for _ in range(4)]:
+            del t
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_of_a_projection_without_outputs(dtype):
+    # n_out = 0: the input's gradient is the empty sum
+    g = gen(83)
+    x, w = randn((37, 200), g, dtype).requires_grad_(True), randn((0, 200), g, dtype).requires_grad_(True)
+    y = fp8.fp8_linear_train(x, w)
+    assert y.shape == (37, 0)
+    leave_nans((37, 200), dtype=dtype)
+    dx, dw = torch.autograd.grad(y.sum(), (x, w))
+    assert dx.shape == x.shape and dx.dtype == dtype and (dx == 0).all() and dw.shape == (0, 200)
+    dh = randn((37, 200), g, dtype)
+    gamma = (1 + 0.3 * randn((200,), g)).to(dtype).requires_grad_(True)
+    h, y = fp8.add_rms_norm_linear(x, None, gamma, 1e-5, w)
+    leave_nans((37, 200), dtype=dtype)
+    dx, dgamma, dw = torch.autograd.grad((h, y), (x, gamma, w), (dh, torch.zeros_like(y)))
+    assert torch.equal(dx, dh) and (dgamma == 0).all() and dw.shape == (0, 200)
+
+
+def test_linear_bwd_without_outputs_zeroes_the_rows_of_dx_only():
+    lib = A.load_library()
+    for dt, dtype in ((0, BF16), (1, F32)):
+        for ld in (40, 43):
+            buf = torch.full((7, ld), 9.0, dtype=dtype, device="cuda")
+            rc = lib.evo_fp8_linear_bwd(6, 0, 40, dt, None, 0, None, 0, None, 0, None, 1, 1, A._ptr(buf), ld, None, 1, 0,
+                                        None, 0, A._stream(buf.device))
+            assert rc == 0
+            assert (buf[:6, :40] == 0).all() and (buf[:6, 40:] == 9).all() and (buf[6:] == 9).all()
+
+
+def test_gradients_without_outputs_in_a_captured_graph():
+    dy = torch.empty((5, 0), dtype=BF16, device="cuda")
+    wq_t, ws_t = fp8.quantize_fp8(torch.empty((0, 64), dtype=BF16, device="cuda"), square=True, transpose=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx = fp8.fp8_linear_bwd(dy, None, wq_t, ws_t, want_dw=False)[0]
+    dx.fill_(9)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (dx == 0).all()
