@@ -20,6 +20,8 @@ over by the gradient.
 """
 from __future__ import annotations
 
+from math import prod
+
 import torch
 from torch.autograd.function import once_differentiable
 
@@ -86,7 +88,7 @@ def _rows(t):
     c = shape[-1]
     t2 = t
     if len(shape) != 2:
-        t2 = t.reshape(t.numel() // c if c else 0, c)
+        t2 = t.reshape(t.numel() // c if c else prod(shape[:-1]), c)
     pitch, step = t2.stride()
     if step != 1 and c > 1:
         t2 = t2.contiguous()

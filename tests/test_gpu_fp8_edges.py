@@ -123,3 +123,23 @@ def test_gradients_without_outputs_in_a_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert (dx == 0).all()
+
+
+def test_leading_axes_of_an_empty_last_axis():
+    g = gen(84)
+    x, w = randn((2, 3, 200), g, BF16).requires_grad_(True), randn((0, 200), g, BF16).requires_grad_(True)
+    y = fp8.fp8_linear_train(x, w)
+    assert y.shape == (2, 3, 0)
+    dx, dw = torch.autograd.grad(y.sum(), (x, w))
+    assert dx.shape == x.shape and (dx == 0).all() and dw.shape == (0, 200)
+    h, y = fp8.add_rms_norm_linear(x, x, None, 1e-5, w)
+    assert h.shape == x.shape and y.shape == (2, 3, 0)
+    dx, dw = torch.autograd.grad((h, y), (x, w), (torch.ones_like(h), torch.zeros_like(y)))
+    assert (dx == 2).all() and dw.shape == (0, 200)
+    e = torch.empty((2, 3, 0), dtype=BF16, device="cuda")
+    q, s = fp8.quantize_fp8(e)
+    assert q.shape == (2, 3, 0) and s.shape == (2, 3, 0)
+    q, s = fp8.quantize_fp8(e, transpose=True)
+    assert q.shape == (0, 6) and s.shape == (0, 1)
+    q, s, qt, st = fp8.quantize_fp8_both(e)
+    assert q.shape == (2, 3, 0) and s.shape == (2, 3, 0) and qt.shape == (0, 6) and st.shape == (0, 1)
