@@ -10,10 +10,11 @@
 // The quotient is rounded once to fp32 before the one rounding to e4m3.  With
 // M = m / 512, t = 0.875 v and inv an approximate 1 / M, q0 = t * inv and the
 // remainder t - q0 * M by a fused multiply-add, q0 + remainder * inv is the
-// rounded quotient (Markstein's correction step; it leaves 2^-22 of a unit in the
+// rounded quotient (Markstein's correction step; it leaves 2^-21 of a unit in the
 // last place).  bf16 values make ties in e4m3 often enough to matter (448 =
 // 7 * 64, so v = 3m/2^k is one); a plain product with 1/m would break them
-// either way.  t is exact for bf16 v and cannot overflow, and neither M nor inv
+// either way.  t is exact for bf16 v (fp32 values have a form of their own) and cannot
+// overflow, and neither M nor inv
 // leaves the normal range.  In the norm the row's 1 / rms cancels out of v / m,
 // so the quotient is that of u = h * weight, exact in fp32 for bf16; its least
 // maximum is LEAST * rms, and rows of a rms so small that its M would be
@@ -68,20 +69,31 @@ struct Divisor {
     __device__ __forceinline__ explicit Divisor(float m) : neg(twice(neg_of(m))), inv(twice(inv_of(m))) {}
     __device__ __forceinline__ Divisor(uint64_t n, uint64_t i) : neg(n), inv(i) {}   // another group for each of the pair
 };
-// 448 * v / m of a pair, rounded.
+// 448 * v / m of a pair, rounded.  EXACT: 0.875 v is a float, as from bf16 values.  Else the remainder
+// is taken in two steps, v - q M and that less v / 8: the first lies near v / 8 and rounds by 2^-27 v,
+// the second is exact, so that the quotient is within 0.65 of a unit in the last place, and exact
+// where it is a float (with 0.875 v rounded it missed ties by a unit; the rounding of 0.875 v carried
+// along takes two more instructions: 131072 x 1024 117 -> 125 us).
+template <bool EXACT>
 __device__ __forceinline__ uint64_t quotient(uint64_t v, const Divisor& d) {
-    const uint64_t t = fmul2(v, twice(0.875f)), q = fmul2(t, d.inv);
-    return ffma2(ffma2(q, d.neg, t), d.inv, q);
+    if constexpr (EXACT) {
+        const uint64_t t = fmul2(v, twice(0.875f)), q = fmul2(t, d.inv);
+        return ffma2(ffma2(q, d.neg, t), d.inv, q);
+    } else {
+        const uint64_t q = fmul2(v, fmul2(d.inv, twice(0.875f)));
+        return ffma2(ffma2(v, twice(-0.125f), ffma2(q, d.neg, v)), d.inv, q);
+    }
 }
-// The same of v + low, the rounding of 0.875 v included: what fp32 values have that bf16 ones do not.
+// The same of v + low: what the norm's fp32 products have beyond v.
 __device__ __forceinline__ uint64_t quotient(uint64_t v, uint64_t low, const Divisor& d) {
     const uint64_t c = twice(0.875f), t = fmul2(v, c), q = fmul2(t, d.inv);
     const uint64_t left = ffma2(c, low, ffma2(c, v, t ^ 0x8000000080000000ull));
     return ffma2(fadd2(ffma2(q, d.neg, t), left), d.inv, q);
 }
 // Four quotients as e4m3 bytes.
+template <bool EXACT>
 __device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b, const Divisor& d) {
-    return e4m3x2(quotient(a, d)) | (e4m3x2(quotient(b, d)) << 16);
+    return e4m3x2(quotient<EXACT>(a, d)) | (e4m3x2(quotient<EXACT>(b, d)) << 16);
 }
 // |v| as an integer that orders like it, with NaN above infinity above the rest:
 // the largest of a group is NaN as soon as one value is.
@@ -258,7 +270,7 @@ template <bool RUN>
 __device__ __forceinline__ void store_e4m3(uint8_t* row, int64_t c0, int64_t cols, int lane, const uint64_t* v,
                                            const float* m, const uint64_t* low = nullptr) {
     auto four = [&](int i, const Divisor& d) {
-        if (!low) return e4m3x4(v[i], v[i + 1], d);
+        if (!low) return e4m3x4<true>(v[i], v[i + 1], d);
         return e4m3x2(quotient(v[i], low[i], d)) | (e4m3x2(quotient(v[i + 1], low[i + 1], d)) << 16);
     };
     const Divisor d0(m[0]);
@@ -764,7 +776,7 @@ __global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !(ROWS && TRANSPO
             for (int i = 0; i < L::TR; i += 4) {
                 uint64_t q[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) q[k] = quotient(t.pair(i + k, j), d);
+                for (int k = 0; k < 4; ++k) q[k] = quotient<L::PACKED>(t.pair(i + k, j), d);
                 tq[L::spot(c, (rr + i) / 4)] = e4m3x2(f2lo(q[0]), f2lo(q[1])) | (e4m3x2(f2lo(q[2]), f2lo(q[3])) << 16);
                 tq[L::spot(c1, (rr + i) / 4)] = e4m3x2(f2hi(q[0]), f2hi(q[1])) | (e4m3x2(f2hi(q[2]), f2hi(q[3])) << 16);
             }
@@ -813,12 +825,12 @@ __global__ void __launch_bounds__(512, Tile<T, VEC>::PACKED && !(ROWS && TRANSPO
 #pragma unroll
             for (int j = 0; j < L::TC / 2; ++j) f[j] = t.pair(i, j);
             if constexpr (L::PACKED) {
-                store_codes(out, c0 + L::col(lane, 0), p.cols, e4m3x4(f[0], f[1], d), e4m3x4(f[2], f[3], d));
+                store_codes(out, c0 + L::col(lane, 0), p.cols, e4m3x4<true>(f[0], f[1], d), e4m3x4<true>(f[2], f[3], d));
             } else if constexpr (VEC) {
                 const int64_t c = c0 + L::col(lane, 0);
-                if (c < p.cols) *reinterpret_cast<uint32_t*>(out + c) = e4m3x4(f[0], f[1], d);
+                if (c < p.cols) *reinterpret_cast<uint32_t*>(out + c) = e4m3x4<false>(f[0], f[1], d);
             } else {
-                const uint32_t b = e4m3x4(f[0], f[1], d);
+                const uint32_t b = e4m3x4<false>(f[0], f[1], d);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int64_t c = c0 + L::col(lane, j);

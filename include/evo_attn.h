@@ -316,9 +316,15 @@ evo_status_t evo_sum_partials(int64_t count, const float* const* parts, int64_t 
  *
  *   code = e4m3(448 * v / m)      scale = m / 448
  *
- * where the quotient is correctly rounded to fp32 and then once to e4m3
- * (nearest, ties to even).  A group that holds a NaN or an infinity gets a
- * NaN scale: its products are NaN, as they would be without rounding.
+ * where the quotient is rounded to fp32 and then once to e4m3 (nearest, ties
+ * to even).  From bf16 values the codes are those of the exact quotient.
+ * From fp32 values the fp32 quotient is within 0.65 of a unit in its last
+ * place, and exact where 448 * v / m is an fp32 number, so that ties go to
+ * even there too.  In the norm v is a product: with an fp32 row or weight it
+ * is rounded, and codes may be neighbours where the quotient lies within
+ * 2^-21 (relative) of a border between two.  A group that holds a NaN or an
+ * infinity gets a NaN scale: its products are NaN, as they would be without
+ * rounding.
  *
  * Codes: rows at a pitch of ld bytes, a multiple of 16, the first 16-byte
  * aligned (else EVO_ERR_UNSUPPORTED); bytes between C and the pitch are never

@@ -143,3 +143,49 @@ def test_leading_axes_of_an_empty_last_axis():
     assert q.shape == (0, 6) and s.shape == (0, 1)
     q, s, qt, st = fp8.quantize_fp8_both(e)
     assert q.shape == (2, 3, 0) and s.shape == (2, 3, 0) and qt.shape == (0, 6) and st.shape == (0, 1)
+
+
+# ------------------------------------------------------------------- rounding of fp32 quotients
+def test_quantize_fp32_breaks_ties_to_even():
+    # m = 7 n and v = (2 j + 1) n 2^e with odd n of 18 bits: 448 v / m = (2 j + 1) 2^(e + 6) lies on a
+    # border for j = 8 .. 15, and 0.875 v has up to 26 bits
+    g = gen(85)
+    n = torch.randint(1 << 17, 1 << 18, (500, 1), generator=g, device="cuda") | 1
+    j = torch.randint(8, 16, (500, 128), generator=g, device="cuda")
+    sign = torch.randint(0, 2, (500, 128), generator=g, device="cuda") * 2.0 - 1
+    e = torch.randint(-7, -2, (500, 128), generator=g, device="cuda")
+    x = sign.double() * (2 * j + 1) * n * torch.tensor([2.0 ** k for k in range(-7, -2)], dtype=torch.float64, device="cuda")[e + 7]
+    x[:, 0] = 7.0 * n[:, 0]
+    assert torch.equal(x, x.float().double()) and (x.abs() <= 7 * n).all()
+    x = x.float()
+    t, m = R.quotients(x, False)
+    assert (R.tie_distance(t)[:, 1:] == 0).float().mean() > 0.9
+    for q, s in (fp8.quantize_fp8(x), fp8.quantize_fp8(x[:, :127].contiguous()), fp8.quantize_fp8_both(x)[:2]):
+        check_codes(q, t[:, : q.shape[1]], 0)
+    q, s = fp8.quantize_fp8(x.t().contiguous(), transpose=True)
+    check_codes(q, t, 0)
+    q, s = fp8.quantize_fp8_both(x.t().contiguous())[2:]
+    check_codes(q, t, 0)
+    one = x[:1].expand(128, 128).contiguous()
+    for q, s in (fp8.quantize_fp8(one, square=True), fp8.quantize_fp8(one.t().contiguous(), square=True, transpose=True)):
+        check_codes(q, t[:1].expand(128, 128), 0)
+
+
+@pytest.mark.parametrize("rows,cols", [(1000, 1024), (257, 1001), (5, 130)])
+def test_quantize_fp32_beside_borders(rows, cols):
+    # values a few units in the last place around the borders of their groups.  The quotient is within
+    # 0.65 of a unit in the last place, at most 2^-23 of the value: neighbours that far from a border only
+    g = gen(rows + cols)
+    x = randn((rows, cols), g)
+    m = R.quotients(x, False)[1].repeat_interleave(128, 1)[:, :cols]
+    code = torch.randint(16, 127, (rows, cols), generator=g, device="cuda", dtype=torch.uint8).view(fp8.CODES).double()
+    up = torch.ldexp(torch.ones_like(code), torch.frexp(code)[1] - 5)    # half a step
+    near = ((code + up) * m / 448).float()
+    near = (near.view(torch.int32) + torch.randint(-3, 4, (rows, cols), generator=g, device="cuda", dtype=torch.int32)).view(F32)
+    x = torch.where((near < m) & (torch.rand((rows, cols), generator=g, device="cuda") < 0.9) & (x.abs() < m), near, x)
+    t, m = R.quotients(x, False)
+    assert (R.tie_distance(t) <= 2.0 ** -21).float().mean() > 0.5
+    for v, kw in ((x, {}), (x.t().contiguous(), {"transpose": True})):
+        q, s = fp8.quantize_fp8(v, **kw)
+        close(s, m / 448, 2.0 ** -23)
+        check_codes(q, t, 0.65 * 2.0 ** -23)
