@@ -189,3 +189,108 @@ def test_quantize_fp32_beside_borders(rows, cols):
         q, s = fp8.quantize_fp8(v, **kw)
         close(s, m / 448, 2.0 ** -23)
         check_codes(q, t, 0.65 * 2.0 ** -23)
+
+
+# ------------------------------------------------------------------- layouts of the product
+@pytest.mark.parametrize("square", [True, False])
+@pytest.mark.parametrize("M,N,K", [(1, 77, 530), (2, 77, 530), (1, 131, 8191), (2, 9, 12345), (1, 1, 17), (2, 257, 128),
+                                   (3, 77, 530), (130, 200, 300), (2000, 1024, 256)])
+def test_linear_layouts_and_neighbours(M, N, K, square):
+    # both operands inside wider rows whose other bytes are NaN codes, scales in either order inside a
+    # wider buffer of NaN, y at odd addresses inside a buffer that stays as it was
+    g = gen(M + N + K)
+    lib = A.load_library()
+    xq, xs, wq, ws = operands(M, N, K, square, g)
+    bias = randn((N,), g)
+
+    def wide(q):
+        buf = torch.full((q.shape[0] + 1, (K + 15) // 16 * 16 + 48), 0x7F, dtype=torch.uint8, device="cuda")
+        buf[:-1, 16:16 + K] = q.contiguous().view(torch.uint8)
+        return buf.view(fp8.CODES)[:-1, 16:16 + K]
+
+    def spread(s, by_group):
+        r, c = s.shape
+        buf = torch.full((c + 2, r + 3) if by_group else (r + 3, c + 2), float("nan"), device="cuda")
+        view = buf[1:-1, 1:-2].t() if by_group else buf[1:-2, 1:-1]
+        view.copy_(s)
+        return view
+
+    for dtype, dt in ((BF16, 0), (F32, 1)):
+        want = fp8.fp8_linear(xq, xs, wq, ws, bias, out_dtype=dtype)
+        check_linear(want, xq, xs, wq, ws, bias)
+        for by_group in (False, True):
+            xw, ww, sx, sw = wide(xq), wide(wq), spread(xs, by_group), spread(ws, by_group)
+            assert torch.equal(want, fp8.fp8_linear(xw, sx, ww, sw, bias, out_dtype=dtype))
+            for off, ld in ((0, N + 8), (1, N + 3)):
+                buf = torch.full(((M + 1) * ld + 1,), 9.0, dtype=dtype, device="cuda")
+                rc = lib.evo_fp8_linear(M, N, K, xw.data_ptr(), xw.stride(0), sx.data_ptr(), sx.stride(0), sx.stride(1),
+                                        ww.data_ptr(), ww.stride(0), sw.data_ptr(), sw.stride(0), sw.stride(1),
+                                        int(not square), A._ptr(bias), dt, buf.data_ptr() + off * buf.element_size(), ld,
+                                        None, 0, A._stream(buf.device))
+                assert rc == 0
+                y = torch.as_strided(buf, (M, N), (ld, 1), off)
+                assert torch.equal(y, want)
+                y.fill_(9.0)
+                assert (buf == 9.0).all()
+
+
+# ------------------------------------------------------------------- long axes
+def test_weight_gradient_over_131072_rows():
+    # quantised along the rows and summed over them: 1024 x 131072 x 256, as for 512 x 256 rows of an MSA
+    g = gen(86)
+    dy, n = stream_rows(131072, 1024, g, BF16), stream_rows(131072, 256, g, BF16)
+    dq, ds = fp8.quantize_fp8(dy, transpose=True)
+    nq, ns = fp8.quantize_fp8(n, transpose=True)
+    for q, s, v in ((dq, ds, dy), (nq, ns, n)):
+        for c0 in range(0, v.shape[1], 256):             # the reference in parts, for its memory
+            part = v[:, c0:c0 + 256].t()
+            t, m = R.quotients(part, False)
+            check_codes(q[c0:c0 + 256], t, 0)
+            close(s[c0:c0 + 256], m / 448, 2.0 ** -23)
+    dw = fp8.fp8_linear(dq, ds, nq, ns, out_dtype=F32)
+    for r0 in range(0, 1024, 256):
+        check_linear(dw[r0:r0 + 256], dq[r0:r0 + 256], ds[r0:r0 + 256], nq, ns, None)
+
+
+def test_projection_of_131072_outputs():
+    g = gen(87)
+    xq, xs, wq, ws = operands(5, 131072, 140, True, g)
+    check_linear(fp8.fp8_linear(xq, xs, wq, ws), xq, xs, wq, ws, None)
+    xq, xs = xq[:1], xs[:1]
+    check_linear(fp8.fp8_linear(xq, xs, wq, ws), xq, xs, wq, ws, None)
+
+
+# ------------------------------------------------------------------- gradients through projection and attention
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_through_norm_projection_and_attention(dtype):
+    """The stream's norm, q/k/v/g in 8 bits, and the attention on views of that output, as one graph."""
+    B, S, N, H, C, D = 1, 3, 24, 2, 32, 96
+    g = gen(88)
+    x, res = (randn((B, S, N, D), g, dtype).requires_grad_(True) for _ in range(2))
+    gamma = (1 + 0.2 * randn((D,), g)).to(dtype).requires_grad_(True)
+    w = (randn((4 * H * C, D), g) / D ** 0.5).to(dtype).requires_grad_(True)
+    pb = randn((B, 1, H, N, N), g, dtype).requires_grad_(True)
+    dout, dh = randn((B, S, N, H, C), g, dtype), randn((B, S, N, D), g, dtype)
+    h, y = fp8.add_rms_norm_linear(x, res, gamma, 1e-5, w)
+    out = A.evoformer_attention(*A.qkvg_views(y, H), None, pb)
+    got = torch.autograd.grad((h, out), (y, x, res, gamma, w, pb), (dh, dout))
+    # the attention's part from its formula in 64 bits, from the same y
+    y64 = y.detach().double().requires_grad_(True)
+    pb64 = pb.detach().double().requires_grad_(True)
+    q, k, v, gate = A.qkvg_views(y64, H)
+    scores = torch.einsum("bsihc,bsjhc->bshij", q, k) / C ** 0.5 + pb64
+    o64 = torch.einsum("bshij,bsjhc->bsihc", scores.softmax(-1), v) * gate.sigmoid()
+    dy64, dpb64 = torch.autograd.grad(o64, (y64, pb64), dout.double())
+    rel = lambda a, b: float((a.detach().double() - b.detach()).norm() / b.detach().norm())  # noqa: E731
+    tol = 5e-3 if dtype == BF16 else 1e-4                # the attention's own tests' bounds
+    assert rel(out, o64) <= tol and rel(got[0], dy64) <= tol and rel(got[-1], dpb64) <= tol
+    # and from there the projection and the norm, from y's gradient as computed
+    dy = got[0].reshape(-1, 4 * H * C)
+    flat = lambda t: t.detach().reshape(-1, D)  # noqa: E731
+    rh, rrstd, rn = R.norm(flat(x), flat(res), gamma.detach(), 1e-5)
+    dn = (R.values(*R.quantize(dy), False) @ R.values(*R.quantize(w.detach(), True), True)).to(dtype)
+    rdx, rdg = R.norm_bwd(dn, flat(dh), rh, rrstd, gamma.detach())
+    rdw = R.values(*R.quantize(dy.t()), False) @ R.values(*R.quantize(rn.to(dtype).t()), False).t()
+    tol = 2.0 ** -8 if dtype == BF16 else 1e-3
+    for a, b in zip(got[1:5], (rdx, rdx, rdg, rdw)):
+        assert rel(a.reshape(b.shape), b) <= tol
