@@ -381,13 +381,15 @@ constexpr int64_t kMaxRowCols = 32768;
 // Forward: as many rows as fit in blocks of 8 warps, two fragments per warp above 2048 columns, up to
 // 16 warps (9763 rows of 4097 columns in fp32: four fragments in five warps took 251 us where this
 // takes 151).
-// Above 8192 columns up to 32 warps of four.
+// Above 8192 columns up to 32 warps of four, whose registers spill (4096 x 12288 in bf16: 162 us, 55 at
+// the copy's rate).
 RowSplit row_split(int64_t cols) {
     const int chunks = (int)((cols + 255) / 256);
     const int nv = chunks <= 8 ? 1 : chunks <= 32 ? 2 : 4, wpr = (chunks + nv - 1) / nv;
     return {nv, wpr, 32 * (wpr <= 8 ? 8 / wpr * wpr : wpr)};
 }
-// Backward: twice the values per column, so one fragment per warp up to 8192 columns.
+// Backward: twice the values per column, so one fragment per warp up to 8192 columns; above, four,
+// which spill (4096 x 12288 in bf16: 281 us, 62 at the copy's rate).
 RowSplit row_split_bwd(int64_t cols) {
     const int chunks = (int)((cols + 255) / 256);
     const int nv = chunks <= 32 ? 1 : 4, wpr = (chunks + nv - 1) / nv;
@@ -564,6 +566,7 @@ struct LinPlan {
 // rows 23.4 and 23.3; four 34.9 and 24).  Else the costs are in blocks of 128 x 256 x 128 on one SM
 // (0.6 us): a block of 128 columns takes as long as one of 256 (both wait more than they add), a
 // CTA's start, last step and end about five, a second launch with its pass over the parts four more.
+// The counts of SMs and of clusters at once are a B200's.
 // Measured both ways: 1024 x 131072 x 256 takes 99 us in clusters of 6, 57 in parts.
 LinPlan plan_linear(int64_t M, int64_t N, int64_t K) {
     namespace f8 = evo::fp8;

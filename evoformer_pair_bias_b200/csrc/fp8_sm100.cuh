@@ -97,13 +97,14 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
 //
 // The summing warps are what bounds the long sums: a block's 128 x BN results are read
 // from TMEM and added in the time the tensor core takes for the next (512 cycles at BN =
-// 256).  Sixteen warps of 64 columns share a tile's way out best: 131072 x 256 x 1024
-// takes 63 us, 71 with eight.  Eight of 128 columns hold twice the registers and need
-// fewer instructions a block: 8191 x 4096 x 8192 takes 301 us back to back under the power
-// cap, 315 with sixteen; 16384 x 1280 x 4096 95 and 98.5; at a sum of 1024 the two are
-// equal (82 us), so that is where Long begins.  The warps hold their sums and nothing that
-// comes from global memory: scales and bias fetched into their own registers spilled and
-// waited for the load at the spill (125 us and 350).
+// 256).  Sixteen warps of 64 columns share a tile's way out best, eight of 128 columns hold
+// twice the registers and need fewer instructions a block.  Both builds in turn on one GPU,
+// calls in a row under the power cap, bf16, us with sixteen and eight: 131072 x 256 x 1024
+// 71.6 and 73.4, 32768 x 1024 x 2048 97.1 and 94.3, 16384 x 1280 x 4096 114.6 and 111.0,
+// 8191 x 4096 x 8192 315 and 303.  Long begins above a sum of 1024, where its gain passes 3 %;
+// from 512 to 1024 eight lead by 1 to 3 %.  The warps hold their sums and nothing that comes
+// from global memory: scales and bias fetched into their own registers spilled and waited for
+// the load at the spill (131072 x 256 x 1024 125 us, 8191 x 4096 x 8192 350).
 constexpr int RING = 8;                                    // blocks whose scales are held
 enum Mode { WHOLE, JOINED, PARTS };
 template <int BN_, int STAGES_, Mode MODE, int WARPS>

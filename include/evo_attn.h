@@ -317,7 +317,9 @@ evo_status_t evo_sum_partials(int64_t count, const float* const* parts, int64_t 
  *   code = e4m3(448 * v / m)      scale = m / 448
  *
  * where the quotient is rounded to fp32 and then once to e4m3 (nearest, ties
- * to even).  From bf16 values the codes are those of the exact quotient.
+ * to even).  From bf16 values the codes are those of the exact quotient (in
+ * the norm but for groups held at the least maximum, whose quotient depends
+ * on rstd).
  * From fp32 values the fp32 quotient is within 0.65 of a unit in its last
  * place, and exact where 448 * v / m is an fp32 number, so that ties go to
  * even there too.  In the norm v is a product: with an fp32 row or weight it
@@ -331,7 +333,8 @@ evo_status_t evo_sum_partials(int64_t count, const float* const* parts, int64_t 
  * written and may hold anything.  Scales: group (r, g) lies at
  * scale[r * scale_row + g * scale_group], r counting rows (1 x 128) or blocks
  * of 128 rows.  Any sizes and any strides; fp32 and bf16 matrices whose rows
- * are 16-byte aligned take 16-byte loads, others single ones.  Stream-ordered,
+ * are 16-byte aligned take 16-byte loads, other bf16 ones words, other fp32
+ * ones single loads.  Stream-ordered,
  * no allocation, no synchronisation.
  */
 
